@@ -199,6 +199,9 @@ def prepare(case, seed):
         st["table"] = torch.tensor(table, device=DEV)
         st["free"] = torch.tensor(order[at[-1]:], dtype=torch.int32, device=DEV)
         st["count"] = torch.tensor([P - int(at[-1])], dtype=torch.int32, device=DEV)
+        if own:
+            import block_sparse_factorized_b200 as bsf
+            st["plan"] = bsf.PagedPlan(R, case["tokens"], DEV)
     else:
         dt = DTYPES[case["dtype"]]
         R, H, KV, d, ps = (case[k] for k in ("requests", "heads", "kv", "d", "page"))
@@ -267,7 +270,7 @@ def _own(st):
         return st["q_out"], st["k_pages"], st["v_pages"]
     if op == "plan":
         p = bsf.st_paged_plan(st["lens"], st["new"], st["table"], st["free"], st["count"], case["page"],
-                              case["tokens"])
+                              case["tokens"], plan=st["plan"])
         return p.lens, p.free_left, p.offsets, p.slots, p.positions, p.status, st["table"]
     return bsf.st_paged_decode(st["q"], st["k_pages"], st["v_pages"], st["table"], st["lens"], st["layout"],
                                workspace=st["workspace"])
