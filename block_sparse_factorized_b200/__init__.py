@@ -10,6 +10,9 @@ library or a non-CUDA tensor is an error.
     lay.upload()
     o, lse = st_attn_fwd(q, k, v, lay)                  # q, k, v: [B, H, n, 64] bf16, CUDA
     dq, dk, dv = st_attn_bwd(q, k, v, o, lse, do, lay)
+
+Beside the factorized patterns it offers operators of language models (lm.py): attention with a
+sliding window and sinks, the norm and rotation of queries and keys, and a paged key/value cache.
 """
 from __future__ import annotations
 
@@ -19,7 +22,7 @@ import numpy as np
 import torch
 
 from . import _abi
-from ._abi import (ST_BF16, ST_ERR_DEVICE_TIMEOUT, ST_FIXED, ST_FP32, ST_KIND_FA1, ST_KIND_FA2, ST_KIND_FU, ST_KIND_SA1,
+from ._abi import (ST_BF16, ST_ERR_BAD_PAGE, ST_ERR_DEVICE_TIMEOUT, ST_FIXED, ST_FP16, ST_FP32, ST_KIND_FA1, ST_KIND_FA2, ST_KIND_FU, ST_KIND_SA1,
                    ST_KIND_SA2, ST_KIND_SU, ST_MERGED, ST_PER_HEAD_ALTERNATING, ST_SINGLE_A1,
                    ST_SINGLE_A2, ST_STRIDED, StError)
 
@@ -28,6 +31,10 @@ __all__ = [
     "st_attn_bwd_workspace_bytes", "SparseAttention", "StError", "ST_ERR_DEVICE_TIMEOUT", "ST_STRIDED", "ST_FIXED",
     "ST_PER_HEAD_ALTERNATING", "ST_MERGED", "ST_SINGLE_A1", "ST_SINGLE_A2", "ST_BF16", "ST_FP32",
     "ST_KIND_SA1", "ST_KIND_SA2", "ST_KIND_SU", "ST_KIND_FA1", "ST_KIND_FA2", "ST_KIND_FU",
+    "ST_FP16", "ST_ERR_BAD_PAGE", "WindowLayout", "st_window_fwd", "st_window_bwd",
+    "st_window_bwd_workspace_bytes", "WindowAttention", "RopeTable", "st_qk_norm_rope", "st_qk_norm_rope_bwd",
+    "st_qk_norm_rope_bwd_workspace_bytes", "QKNormRope", "PagedPlan", "st_paged_plan", "st_paged_append",
+    "st_paged_decode", "st_paged_decode_workspace_bytes",
 ]
 
 _c = ctypes
@@ -277,3 +284,9 @@ class SparseAttention(torch.autograd.Function):
         q, k, v, o, lse = ctx.saved_tensors
         dq, dk, dv = st_attn_bwd(q, k, v, o, lse, do.contiguous(), ctx.layout)
         return dq, dk, dv, None
+
+
+from .lm import (PagedPlan, QKNormRope, RopeTable, WindowAttention, WindowLayout, st_paged_append,  # noqa: E402
+                 st_paged_decode, st_paged_decode_workspace_bytes, st_paged_plan, st_qk_norm_rope,
+                 st_qk_norm_rope_bwd, st_qk_norm_rope_bwd_workspace_bytes, st_window_bwd,
+                 st_window_bwd_workspace_bytes, st_window_fwd)

@@ -4,13 +4,15 @@
 #include <math.h>
 #include <string.h>
 
-#include <atomic>
-
 #include "decode.h"
 #include "kernels.h"
 #include "layout.h"
+#include "tensor_map.h"
 
 namespace {
+
+using st::encode;
+using st::encode_fn;
 
 // Forward workspace head: one int32 unit counter per pass (zeroed by every call), padded so the
 // fp32 copies that follow stay 256-byte aligned.
@@ -30,42 +32,6 @@ size_t bwd_partial_bytes(const st_desc_t *desc, const st_layout_t *layout)
 size_t bwd_counter_bytes(const st_desc_t *, const st_layout_t *)
 {
     return 2 * sizeof(int32_t);
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn lookup_encode()
-{
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-        return reinterpret_cast<EncodeTiledFn>(ptr);
-    return nullptr;
-}
-
-// The driver's tensor-map encoder, looked up once (thread-safe static initialisation; a failed
-// lookup is retried by the next call).
-EncodeTiledFn encode_fn()
-{
-    static std::atomic<EncodeTiledFn> fn{lookup_encode()};
-    EncodeTiledFn f = fn.load(std::memory_order_acquire);
-    if (!f && (f = lookup_encode())) fn.store(f, std::memory_order_release);
-    return f;
-}
-
-bool encode(CUtensorMap *m, const void *base, CUtensorMapDataType dt, cuuint32_t rank,
-            const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
-            CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B)
-{
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    return encode_fn()(m, dt, rank, const_cast<void *>(base), dims, strides, box, es,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Tensor maps of a bf16 [BH, n, W] tensor in the natural, grid-column and summary frames.  A box
@@ -590,6 +556,7 @@ const char *st_status_string(st_status_t s)
     case ST_ERR_DEVICE_TIMEOUT: return "device wait timed out";
     case ST_ERR_WORKSPACE: return "workspace missing or too small";
     case ST_ERR_INTERNAL: return "internal error";
+    case ST_ERR_BAD_PAGE: return "block table names a page outside the cache";
     }
     return "unknown status";
 }

@@ -1,0 +1,479 @@
+"""Operators of language models: attention with a sliding window and sinks, per-head norms of queries
+and keys with the position rotation, and a paged key/value cache.
+
+The bindings of the second half of include/st_attn.h, same names; they marshal tensors (with their
+strides) into the C calls.  As elsewhere in the package there is no CPU path.  Calls are
+asynchronous on ``stream`` (default: the current stream of the inputs' device).
+
+    win = WindowLayout(heads=16, kv_heads=4, window=1024, sinks=16).upload()
+    rope = RopeTable(128, scaling="yarn", factor=16, original=8192, device="cuda")
+    # training: norm + rotation, attention, both with gradients
+    q, k = QKNormRope.apply(q, k, wq, wk, rope)
+    o = WindowAttention.apply(q, k, v, win)
+    # serving: plan the step, store the new tokens, attend over the pages
+    plan = st_paged_plan(lens, new, block_table, free_pages, free_count, page_size, tokens)
+    q = st_paged_append(q, k, v, rope, plan.slots, plan.positions, k_pages, v_pages, wq=wq, wk=wk)
+    o, lse = st_paged_decode(q, k_pages, v_pages, block_table, plan.lens, win)
+"""
+from __future__ import annotations
+
+import ctypes as _c
+
+import torch
+
+from . import _abi
+
+_DTYPES = {torch.bfloat16: _abi.ST_BF16, torch.float16: _abi.ST_FP16, torch.float32: _abi.ST_FP32}
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+class _On:
+    """The inputs' device made current for the call, and the stream to launch on."""
+
+    def __init__(self, device, stream):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        if stream is None:
+            stream = torch.cuda.current_stream(device).cuda_stream
+        elif isinstance(stream, torch.cuda.Stream):
+            if stream.device != device:
+                raise ValueError("the stream belongs to another device than the tensors")
+            stream = stream.cuda_stream
+        self.stream = _c.c_void_p(int(stream))
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _dtype(t):
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _check(name, t, shape, dtype, device):
+    """A CUDA tensor of this shape, type and device whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {device}, not {tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _check_flat(name, t, shape, dtype, device):
+    _check(name, t, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _strides(t):
+    return _abi.st_strides_t(t.stride(0), t.stride(1), t.stride(2))
+
+
+def _token_strides(t):
+    """[tokens, heads, d] as [1, heads, tokens, d]."""
+    return _abi.st_strides_t(0, t.stride(1), t.stride(0))
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(ws, need, device):
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    if not ws.is_cuda or ws.device != device or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the inputs' device")
+    return ws
+
+
+def _nbytes(ws):
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+# ---- sliding-window attention -----------------------------------------------------------------
+class WindowLayout:
+    """Owner of an st_window_t: query position p sees the keys j <= p with j > p - window (0: no
+    limit) or j < sinks; head h reads key head h // (heads // kv_heads)."""
+
+    def __init__(self, heads: int, kv_heads: int, window: int, sinks: int = 0):
+        self._lib = _abi.load()
+        self._h = _c.c_void_p()
+        _abi.check(self._lib.st_window_create(heads, kv_heads, window, sinks, _c.byref(self._h)), "st_window_create")
+        self.heads, self.kv_heads, self.window, self.sinks = heads, kv_heads, window, sinks
+
+    @property
+    def handle(self):
+        return self._h
+
+    def upload(self, device=None, stream=None) -> "WindowLayout":
+        """Bind to ``device`` (default: the current one)."""
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        with _On(device, stream) as s:
+            _abi.check(self._lib.st_window_upload(self._h, s), "st_window_upload")
+        self.device = device
+        return self
+
+    def check(self, stream=None) -> None:
+        """Synchronise and raise StError for a device wait that ran out (ST_ERR_DEVICE_TIMEOUT) or a
+        page outside the cache (ST_ERR_BAD_PAGE) since the last check."""
+        with _On(getattr(self, "device", torch.device("cuda", torch.cuda.current_device())), stream) as s:
+            _abi.check(self._lib.st_window_check(self._h, s), "st_window_check")
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and h.value:
+            self._lib.st_window_destroy(h)
+            h.value = None
+
+
+def _window_desc(q, k, v, layout, q_start, lens):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("expected [batch, heads, n, d] tensors")
+    B, H, nq, d = q.shape
+    nk = k.shape[2]
+    _check("q", q, (B, layout.heads, nq, d), q.dtype, q.device)
+    for name, t in (("k", k), ("v", v)):
+        _check(name, t, (B, layout.kv_heads, nk, d), q.dtype, q.device)
+    if lens is not None:
+        _check_flat("lens", lens, (B,), torch.int32, q.device)
+    if q_start is None:
+        q_start = nk - nq
+        if q_start < 0:
+            raise ValueError("more queries than keys: give q_start")
+    desc = _abi.st_window_desc_t(B, nq, nk, d, q_start, _dtype(q), 0)
+    desc.q, desc.k, desc.v = _strides(q), _strides(k), _strides(v)
+    return desc
+
+
+def st_window_fwd(q, k, v, layout: WindowLayout, q_start=None, lens=None, o=None, lse=None, stream=None, check=False):
+    """O [B, H, nq, d] and lse [B, H, nq] (fp32, natural log) of sliding-window attention.
+
+    q: [B, H, nq, d]; k, v: [B, KV, nk, d] (bf16 or fp16, d 64 or 128, any strides with contiguous
+    rows).  Row i stands at position q_start + i (default: the last nq of nk).  lens: int32 [B]
+    lengths of a padded batch; rows and keys at lens[b] and beyond are padding (O = 0, lse = -inf).
+    Asynchronous: ``layout.check()`` or ``check=True`` reports a device wait that ran out."""
+    desc = _window_desc(q, k, v, layout, q_start, lens)
+    if o is None:
+        o = torch.empty_like(q)
+    _check("o", o, q.shape, q.dtype, q.device)
+    if lse is None:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    _check_flat("lse", lse, q.shape[:3], torch.float32, q.device)
+    desc.o = _strides(o)
+    with _On(q.device, stream) as s:
+        _abi.check(layout._lib.st_window_fwd(_p(q), _p(k), _p(v), _p(lens), layout.handle, _p(o), _p(lse),
+                                             _c.byref(desc), s), "st_window_fwd")
+    if check:
+        layout.check(stream)
+    return o, lse
+
+
+def st_window_bwd_workspace_bytes(q, k, layout: WindowLayout, q_start=None) -> int:
+    desc = _window_desc(q, k, k, layout, q_start, None)
+    with _On(q.device, None):
+        return int(layout._lib.st_window_bwd_workspace_bytes(_c.byref(desc), layout.handle))
+
+
+def st_window_bwd(q, k, v, o, lse, do, layout: WindowLayout, q_start=None, lens=None, dq=None, dk=None, dv=None,
+                  workspace=None, stream=None, check=False):
+    """dQ, dK, dV of st_window_fwd (recomputing P from the saved lse); deterministic."""
+    desc = _window_desc(q, k, v, layout, q_start, lens)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    for name, t, like in (("o", o, q), ("do", do, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _check(name, t, like.shape, q.dtype, q.device)
+    _check_flat("lse", lse, q.shape[:3], torch.float32, q.device)
+    desc.o, desc.dout = _strides(o), _strides(do)
+    desc.dq, desc.dk, desc.dv = _strides(dq), _strides(dk), _strides(dv)
+    with _On(q.device, stream) as s:
+        need = layout._lib.st_window_bwd_workspace_bytes(_c.byref(desc), layout.handle)
+        workspace = _workspace(workspace, need, q.device)
+        _abi.check(layout._lib.st_window_bwd(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(do), _p(lens), layout.handle,
+                                             _p(dq), _p(dk), _p(dv), _p(workspace), _nbytes(workspace),
+                                             _c.byref(desc), s), "st_window_bwd")
+    if check:
+        layout.check(stream)
+    return dq, dk, dv
+
+
+def _rows(t):
+    return t if t.shape[-1] == 1 or t.stride(-1) == 1 else t.contiguous()
+
+
+def _as_rows(t):
+    """A gradient as the kernels read it: contiguous rows on 16-byte boundaries (an expanded one, as of
+    a sum, has strides of 0)."""
+    es = t.element_size()
+    ok = t.data_ptr() % 16 == 0 and t.stride(-1) == 1 and all(
+        t.shape[i] == 1 or (t.stride(i) >= t.shape[-1] and t.stride(i) * es % 16 == 0) for i in range(t.dim() - 1))
+    return t if ok else t.contiguous()
+
+
+class WindowAttention(torch.autograd.Function):
+    """Autograd wrapper: apply(q, k, v, layout, lens=None, q_start=None) -> o.
+
+    To capture a training step into a CUDA graph, hold no autograd graph of the same leaves from
+    outside the capture while it runs (PyTorch would wait across the capture's streams); calls of
+    st_window_fwd and st_window_bwd themselves may be captured at any time."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, layout, lens=None, q_start=None):
+        o, lse = st_window_fwd(q, k, v, layout, q_start=q_start, lens=lens)
+        ctx.save_for_backward(q, k, v, o, lse, lens)
+        ctx.layout, ctx.q_start = layout, q_start
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, o, lse, lens = ctx.saved_tensors
+        dq, dk, dv = st_window_bwd(q, k, v, o, lse, _as_rows(do), ctx.layout, q_start=ctx.q_start, lens=lens)
+        return dq, dk, dv, None, None, None
+
+
+# ---- norm and rotation ------------------------------------------------------------------------
+class RopeTable:
+    """Rotation speeds of the first ``rot`` elements of a head (made once per model).
+
+    scaling: "none", "linear", "ntk" or "yarn", by ``factor`` for contexts that many times the
+    ``original`` one (st_rope_turns gives the formulas); interleaved: pairs (2i, 2i + 1), else
+    (i, i + rot / 2)."""
+
+    def __init__(self, rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 original: float = 8192, interleaved: bool = False, device="cuda"):
+        if scaling not in _SCALINGS:
+            raise ValueError(f"unknown scaling {scaling!r}: one of {', '.join(_SCALINGS)}")
+        turns = torch.empty(max(rot // 2, 1), dtype=torch.float64)
+        mscale = _c.c_float()
+        _abi.check(_abi.load().st_rope_turns(rot, base, _SCALINGS[scaling], factor, original,
+                                             _c.cast(turns.data_ptr(), _c.POINTER(_c.c_double)), _c.byref(mscale)),
+                   "st_rope_turns")
+        self.rot, self.interleaved, self.mscale = rot, bool(interleaved), mscale.value
+        self.turns = turns.to(device)
+
+
+def _rope_desc(q, k, rope, wq, wk, eps, positions, start, token_major):
+    """q, k: [B, H, n, d] and [B, KV, n, d], or packed [n, H, d] and [n, KV, d] (token_major)."""
+    if q.dim() != (3 if token_major else 4) or k.dim() != q.dim():
+        raise ValueError("expected [tokens, heads, d] tensors" if token_major else "expected [batch, heads, n, d] tensors")
+    if token_major:
+        (n, H, d), B, KV = q.shape, 1, k.shape[1]
+        kshape = (n, KV, d)
+    else:
+        (B, H, n, d), KV = q.shape, k.shape[1]
+        kshape = (B, KV, n, d)
+    _check("q", q, q.shape, q.dtype, q.device)
+    _check("k", k, kshape, q.dtype, q.device)
+    if (wq is None) != (wk is None):
+        raise ValueError("give both norm weights or neither")
+    wdt = _dtype(q)
+    if wq is not None:
+        for name, w in (("wq", wq), ("wk", wk)):
+            _check_flat(name, w, (d,), wq.dtype, q.device)
+        if wq.dtype not in (torch.float32, q.dtype):
+            raise TypeError("norm weights must be fp32 or of the queries' type")
+        wdt = _dtype(wq)
+    if rope.turns.device != q.device:
+        raise ValueError("the rotation table is on another device")
+    pos_batch = 0
+    if positions is not None:
+        shape = (n,) if positions.dim() == 1 else (B, n)
+        _check_flat("positions", positions, shape, torch.int32, q.device)
+        pos_batch = n if positions.dim() == 2 else 0
+    desc = _abi.st_rope_desc_t(B, H, KV, n, d, start, pos_batch, rope.rot, int(rope.interleaved), _dtype(q), wdt,
+                               eps, rope.mscale)
+    st = _token_strides if token_major else _strides
+    desc.q, desc.k = st(q), st(k)
+    return desc
+
+
+def st_qk_norm_rope(q, k, rope: RopeTable, wq=None, wk=None, eps: float = 1e-6, positions=None, start: int = 0,
+                    q_out=None, k_out=None, stream=None):
+    """Per-head RMS norm of q [B, H, n, d] and k [B, KV, n, d] (weights [d], or no norm) and their
+    rotation, in one pass; returns (q_out, k_out), contiguous unless given (q_out may be q).
+    Positions are positions ([n] or [B, n] int32), or start, start + 1, ..."""
+    desc = _rope_desc(q, k, rope, wq, wk, eps, positions, start, False)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+    _check("q_out", q_out, q.shape, q.dtype, q.device)
+    _check("k_out", k_out, k.shape, q.dtype, q.device)
+    desc.q_out, desc.k_out = _strides(q_out), _strides(k_out)
+    with _On(q.device, stream) as s:
+        _abi.check(_abi.load().st_qk_norm_rope(_p(q), _p(k), _p(wq), _p(wk), _p(rope.turns), _p(positions), _p(q_out),
+                                               _p(k_out), _c.byref(desc), s), "st_qk_norm_rope")
+    return q_out, k_out
+
+
+def _rope_bwd_need(desc):
+    return int(_abi.load().st_qk_norm_rope_bwd_workspace_bytes(_c.byref(desc)))
+
+
+def st_qk_norm_rope_bwd_workspace_bytes(q, k, rope: RopeTable) -> int:
+    with _On(q.device, None):
+        return _rope_bwd_need(_rope_desc(q, k, rope, None, None, 0.0, None, 0, False))
+
+
+def st_qk_norm_rope_bwd(q, k, gq, gk, rope: RopeTable, wq=None, wk=None, eps: float = 1e-6, positions=None,
+                        start: int = 0, dq=None, dk=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dwq, dwk) for the output gradients gq, gk; dwq and dwk are fp32, or None
+    without weights.  dq may be gq and dk may be gk."""
+    desc = _rope_desc(q, k, rope, wq, wk, eps, positions, start, False)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    for name, t, like in (("gq", gq, q), ("gk", gk, k), ("dq", dq, q), ("dk", dk, k)):
+        _check(name, t, like.shape, q.dtype, q.device)
+    desc.q_out, desc.k_out, desc.dq, desc.dk = _strides(gq), _strides(gk), _strides(dq), _strides(dk)
+    dwq = dwk = None
+    with _On(q.device, stream) as s:
+        if wq is not None:
+            dw = torch.empty((2, q.shape[-1]), dtype=torch.float32, device=q.device)
+            dwq, dwk = dw[0], dw[1]
+            workspace = _workspace(workspace, _rope_bwd_need(desc), q.device)
+        _abi.check(_abi.load().st_qk_norm_rope_bwd(_p(q), _p(k), _p(gq), _p(gk), _p(wq), _p(wk), _p(rope.turns),
+                                                   _p(positions), _p(dq), _p(dk), _p(dwq), _p(dwk), _p(workspace),
+                                                   _nbytes(workspace), _c.byref(desc), s), "st_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+class QKNormRope(torch.autograd.Function):
+    """Autograd wrapper: apply(q, k, wq, wk, rope, eps=1e-6, positions=None, start=0) -> (q, k).
+    Under CUDA graph capture the note of WindowAttention holds."""
+
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, rope, eps=1e-6, positions=None, start=0):
+        ctx.save_for_backward(q, k, wq, wk, positions)
+        ctx.rope, ctx.eps, ctx.start = rope, eps, start
+        return st_qk_norm_rope(q, k, rope, wq=wq, wk=wk, eps=eps, positions=positions, start=start)
+
+    @staticmethod
+    def backward(ctx, gq, gk):
+        q, k, wq, wk, positions = ctx.saved_tensors
+        dq, dk, dwq, dwk = st_qk_norm_rope_bwd(q, k, _as_rows(gq), _as_rows(gk), ctx.rope, wq=wq, wk=wk, eps=ctx.eps,
+                                               positions=positions, start=ctx.start)
+        if wq is not None:
+            dwq, dwk = dwq.to(wq.dtype), dwk.to(wk.dtype)
+        return dq, dk, dwq, dwk, None, None, None, None
+
+
+# ---- paged cache ------------------------------------------------------------------------------
+class PagedPlan:
+    """Outputs of st_paged_plan for up to ``tokens`` new tokens of ``requests`` requests, all int32:
+    lens [requests], free_left [1], offsets [requests + 1], slots and positions [tokens], status
+    [requests].  A program may keep one and plan into it every step."""
+
+    def __init__(self, requests: int, tokens: int, device="cuda"):
+        self.requests, self.tokens = requests, tokens
+        sizes = (requests, 1, requests + 1, tokens, tokens, requests)
+        at = [0]
+        for n in sizes:
+            at.append(at[-1] + (n + 63) // 64 * 64)
+        buf = torch.empty(at[-1], dtype=torch.int32, device=device)
+        self.device = buf.device
+        (self.lens, self.free_left, self.offsets, self.slots, self.positions,
+         self.status) = (buf[a:a + n] for a, n in zip(at, sizes))
+
+
+def st_paged_plan(lens, new, block_table, free_pages, free_count, page_size: int, tokens: int, plan: PagedPlan = None,
+                  stream=None) -> PagedPlan:
+    """Plan a serving step on the device: lens, new [requests], block_table [requests, max_pages]
+    (newly taken pages are written in place), free_pages [*] with free_count [1] of them free, all
+    int32.  ``tokens`` is the room for new tokens; entries past the last one are -1."""
+    device = lens.device
+    if lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("expected lens [requests], block_table [requests, max_pages] and free_pages [*]")
+    R = lens.shape[0]
+    i32 = torch.int32
+    _check_flat("lens", lens, (R,), i32, device)
+    _check_flat("new", new, (R,), i32, device)
+    _check("block_table", block_table, (R, block_table.shape[1]), i32, device)
+    _check_flat("free_pages", free_pages, free_pages.shape, i32, device)
+    _check_flat("free_count", free_count, (1,), i32, device)
+    if plan is None:
+        plan = PagedPlan(R, tokens, device)
+    elif plan.requests != R or plan.tokens != tokens or plan.device != device:
+        raise ValueError("plan was made for other sizes or another device")
+    desc = _abi.st_plan_desc_t(R, tokens, block_table.shape[1], block_table.stride(0), page_size, free_pages.shape[0])
+    with _On(device, stream) as s:
+        _abi.check(_abi.load().st_paged_plan(_p(lens), _p(new), _p(block_table), _p(free_pages), _p(free_count),
+                                             _p(plan.lens), _p(plan.free_left), _p(plan.offsets), _p(plan.slots),
+                                             _p(plan.positions), _p(plan.status), _c.byref(desc), s), "st_paged_plan")
+    return plan
+
+
+def _pages(k_pages, v_pages, kv, d, dtype, device):
+    if k_pages.dim() != 4:
+        raise ValueError("pages must be [num_pages, kv_heads, page_size, d]")
+    P, _, ps, _ = k_pages.shape
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _check(name, t, (P, kv, ps, d), dtype, device)
+    return _abi.st_pages_t(P, ps, _strides(k_pages), _strides(v_pages))
+
+
+def st_paged_append(q, k, v, rope: RopeTable, slots, positions, k_pages, v_pages, wq=None, wk=None, eps: float = 1e-6,
+                    q_out=None, stream=None):
+    """New tokens into the cache: q [tokens, H, d] is normed and rotated into q_out, k [tokens, KV, d]
+    likewise into its slot of k_pages, v into v_pages ([num_pages, KV, page_size, d] each).  Tokens
+    with slot -1 are skipped: their rows of q_out stay as they were (a q_out made here has them 0)."""
+    desc = _rope_desc(q, k, rope, wq, wk, eps, positions, 0, True)
+    n, KV, d = k.shape
+    _check("v", v, k.shape, q.dtype, q.device)
+    _check_flat("slots", slots, (n,), torch.int32, q.device)
+    if positions is None or positions.dim() != 1:
+        raise ValueError("positions must be [tokens]")
+    pages = _pages(k_pages, v_pages, KV, d, q.dtype, q.device)
+    q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    _check("q_out", q_out, q.shape, q.dtype, q.device)
+    desc.q_out = _token_strides(q_out)
+    vs = _token_strides(v)
+    with _On(q.device, stream) as s:
+        _abi.check(_abi.load().st_paged_append(_p(q), _p(k), _p(v), _p(wq), _p(wk), _p(rope.turns), _p(positions),
+                                               _p(slots), _p(q_out), _p(k_pages), _p(v_pages), _c.byref(vs),
+                                               _c.byref(pages), _c.byref(desc), s), "st_paged_append")
+    return q_out
+
+
+def st_paged_decode_workspace_bytes(q, layout: WindowLayout) -> int:
+    """Bytes for any decode call of q's shape [requests, H, d] with this layout."""
+    s = _abi.st_strides_t(0, q.shape[2], q.shape[2])
+    desc = _abi.st_paged_desc_t(q.shape[0], q.shape[2], 1, 1, _dtype(q), 0, _abi.st_pages_t(1, 16, s, s))
+    with _On(q.device, None):
+        return int(layout._lib.st_paged_decode_workspace_bytes(_c.byref(desc), layout.handle))
+
+
+def st_paged_decode(q, k_pages, v_pages, block_table, lens, layout: WindowLayout, o=None, lse=None, workspace=None,
+                    stream=None, check=False):
+    """One new token per request over its pages: q [requests, H, d] at position lens - 1 against the
+    keys of block_table [requests, max_pages] (int32), behind the layout's window and sinks.  Returns
+    o [requests, H, d] and lse [requests, H]; a request of length 0 gets O = 0, lse = -inf.
+    Asynchronous: ``layout.check()`` or ``check=True`` reports a page outside the cache."""
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("expected q [requests, heads, d] and block_table [requests, max_pages]")
+    R, H, d = q.shape
+    _check_flat("q", q, (R, layout.heads, d), q.dtype, q.device)
+    pages = _pages(k_pages, v_pages, layout.kv_heads, d, q.dtype, q.device)
+    _check("block_table", block_table, (R, block_table.shape[1]), torch.int32, q.device)
+    _check_flat("lens", lens, (R,), torch.int32, q.device)
+    o = torch.empty_like(q) if o is None else o
+    lse = torch.empty((R, H), dtype=torch.float32, device=q.device) if lse is None else lse
+    _check_flat("o", o, q.shape, q.dtype, q.device)
+    _check_flat("lse", lse, (R, H), torch.float32, q.device)
+    desc = _abi.st_paged_desc_t(R, d, block_table.shape[1], block_table.stride(0), _dtype(q), 0, pages)
+    with _On(q.device, stream) as s:
+        if workspace is None:
+            need = layout._lib.st_paged_decode_workspace_bytes(_c.byref(desc), layout.handle)
+        workspace = _workspace(workspace, need if workspace is None else 0, q.device)
+        _abi.check(layout._lib.st_paged_decode(_p(q), _p(k_pages), _p(v_pages), _p(block_table), _p(lens), layout.handle,
+                                               _p(o), _p(lse), _p(workspace), _nbytes(workspace), _c.byref(desc), s),
+                   "st_paged_decode")
+    if check:
+        layout.check(stream)
+    return o, lse

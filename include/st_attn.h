@@ -59,7 +59,8 @@ typedef enum {
     ST_ERR_OOM = 6,             /* host or device allocation failed */
     ST_ERR_DEVICE_TIMEOUT = 7,  /* a bounded device wait gave up (see st_layout_check) */
     ST_ERR_WORKSPACE = 8,       /* workspace NULL or smaller than the *_workspace_bytes figure */
-    ST_ERR_INTERNAL = 9
+    ST_ERR_INTERNAL = 9,
+    ST_ERR_BAD_PAGE = 10        /* a block table named a page outside the cache (st_window_check) */
 } st_status_t;
 
 typedef enum { ST_STRIDED = 1, ST_FIXED = 2 } st_family_t;
@@ -86,7 +87,9 @@ typedef struct {
     int32_t a2_offset_step; /* <= 0: c */
 } st_pattern_t;
 
-typedef enum { ST_BF16 = 1, ST_FP32 = 2 } st_dtype_t;
+/* ST_FP16 is taken by the window, norm-and-rotation and paged calls below; the factorized patterns'
+ * calls (st_attn_*) refuse it with ST_ERR_INVALID_ARG. */
+typedef enum { ST_BF16 = 1, ST_FP32 = 2, ST_FP16 = 3 } st_dtype_t;
 
 /* Shapes of one call.  Q, K, dQ, dK are [batch, heads, n, d]; V, O, dO, dV are
  * [batch, heads, n, dv] ("Sparse Transformers 深度解读报告" §4.5: the models' per-head widths
@@ -298,6 +301,196 @@ ST_API st_status_t st_attn_decode(const void *q, const void *k_cache, const void
  * decode step's key sets against the set definitions. */
 ST_API st_status_t st_decode_row_keys(const st_layout_t *layout, int32_t head, int64_t pos,
                                       int64_t *keys, int64_t *count);
+
+/* ================================================================================================
+ * Operators of language models: attention with a sliding window and sinks, per-head norms with
+ * the position rotation, and a paged key/value cache.  They share these conventions:
+ *   - Tensors are given with element strides (st_strides_t); the innermost dimension is contiguous.
+ *     Pointers are 16-byte aligned and every stride of a dimension longer than 1 is positive and a
+ *     multiple of 16 bytes (ST_ERR_ALIGNMENT otherwise; a stride of 0 or below: ST_ERR_INVALID_ARG).
+ *     Elements of one tensor do not overlap, and outputs do not overlap inputs or each other unless
+ *     a call says so.
+ *   - Each handle belongs to the device current at its upload; calls are made with that device
+ *     current (ST_ERR_INVALID_ARG otherwise).
+ *   - Nothing is allocated and nothing is kept between calls: a call may be captured into a CUDA
+ *     graph.  Calls whose work overlaps on the GPU need separate workspaces.
+ * ================================================================================================ */
+
+/* Element strides of a [batch, heads, rows, width] tensor. */
+typedef struct {
+    int64_t batch, head, row;
+} st_strides_t;
+
+/* A sliding window with sinks.  A query at position p sees the keys j with
+ *     j <= p  and  (window == 0  or  j > p - window  or  j < sinks):
+ * the last `window` positions, its own included (0: the whole past), and the first `sinks`.
+ * Query heads share key heads in groups: head h reads key head h / (heads / kv_heads). */
+typedef struct st_window st_window_t;
+
+/* heads, kv_heads >= 1 with heads % kv_heads == 0; window, sinks in 0 .. 2^30 (host only). */
+ST_API st_status_t st_window_create(int32_t heads, int32_t kv_heads, int64_t window, int64_t sinks,
+                                    st_window_t **out);
+/* Bind the handle to the current device and allocate its error word (the only allocation). */
+ST_API st_status_t st_window_upload(st_window_t *window, st_stream_t stream);
+/* Synchronise `stream`, report and clear the handle's device error word: ST_ERR_DEVICE_TIMEOUT if
+ * a bounded wait gave up, ST_ERR_BAD_PAGE if a block table named a page outside the cache.  The
+ * error word is shared by every call made with the handle, on any stream. */
+ST_API st_status_t st_window_check(st_window_t *window, st_stream_t stream);
+/* Release the handle (NULL is a no-op).  Work that uses it must have completed. */
+ST_API void st_window_destroy(st_window_t *window);
+
+/* Shapes of a window call.  q, o, dO, dq: [batch, heads, nq, d]; k, v, dk, dv: [batch, kv_heads,
+ * nk, d]; lse: [batch, heads, nq] fp32, contiguous.  Query row i stands at position q_start + i of
+ * the keys' sequence.  Scores are scaled by 1 / sqrt(d).  d: 64 or 128; dtype: ST_BF16 or ST_FP16;
+ * nq, nk <= 2^30; q_start + nq <= 2^30 (others: ST_ERR_UNSUPPORTED). */
+typedef struct {
+    int64_t batch, nq, nk, d, q_start;
+    int32_t dtype, reserved;
+    st_strides_t q, k, v, o, dout, dq, dk, dv; /* the forward reads q, k, v, o only */
+} st_window_desc_t;
+
+/* Forward: O_i = sum_j softmax_j(q_i . k_j / sqrt d) v_j over the keys that row i sees, and
+ * lse_i = ln sum_j exp(q_i . k_j / sqrt d).
+ *   lens  device int32 [batch] or NULL: the sequence of batch element b has lens[b] positions
+ *         (clamped to 0 .. nk; NULL: nk).  Rows at positions lens[b] and beyond are padding: O = 0
+ *         and lse = -inf; keys there are not seen, whatever they hold (NaN included).
+ * A NaN or an infinity in a row before lens[b] may reach any row of its batch element and group.
+ * 16-bit products with fp32 accumulation; the probabilities are rounded to the inputs' type for
+ * the second product.
+ * Errors: ST_ERR_INVALID_ARG (NULL pointer, sizes, q_start < 0, another device current),
+ * ST_ERR_UNSUPPORTED, ST_ERR_ALIGNMENT, ST_ERR_NOT_UPLOADED, ST_ERR_CUDA. */
+ST_API st_status_t st_window_fwd(const void *q, const void *k, const void *v, const int32_t *lens,
+                                 const st_window_t *window, void *o, float *lse,
+                                 const st_window_desc_t *desc, st_stream_t stream);
+
+/* Backward with recomputation from q, k and the saved lse: dq, dk, dv (every element written;
+ * padding rows and unseen keys get 0, whatever dO, O and lse hold there).  The sums run in a fixed
+ * order: the same inputs give the same bits.  dS (and P) are rounded to the inputs' type for their
+ * products; with ST_FP16 they are scaled by powers of two that keep them in range, per key head.
+ * Errors as for the forward, and ST_ERR_WORKSPACE. */
+ST_API size_t st_window_bwd_workspace_bytes(const st_window_desc_t *desc, const st_window_t *window);
+ST_API st_status_t st_window_bwd(const void *q, const void *k, const void *v, const void *o,
+                                 const float *lse, const void *dO, const int32_t *lens,
+                                 const st_window_t *window, void *dq, void *dk, void *dv,
+                                 void *workspace, size_t workspace_bytes, const st_window_desc_t *desc,
+                                 st_stream_t stream);
+
+/* ---- norms of queries and keys per head, with the position rotation -------------------------- */
+typedef enum { ST_ROPE_NONE = 0, ST_ROPE_LINEAR = 1, ST_ROPE_NTK = 2, ST_ROPE_YARN = 3 } st_rope_scaling_t;
+
+/* Rotation speeds (host only): turns[i] = w_i / 2 pi, i < rot / 2, in turns per position, with
+ * w_i = base^(-2i / rot), and the factor *mscale on cos and sin (1 except for YARN).  Scaling by
+ * `factor` s >= 1 for contexts s times the `original` one:
+ *   LINEAR  w_i / s (positions interpolated)
+ *   NTK     base s^(rot / (rot - 2)): the slowest pair slows by s, the fastest keeps its speed
+ *   YARN    by parts: r_i = original w_i / 2 pi turns over the original context, kept share
+ *           t = clamp((r_i - 1) / (32 - 1), 0, 1), w_i (t + (1 - t) / s); mscale = 0.1 ln s + 1
+ * Errors: ST_ERR_INVALID_ARG (NULL, rot odd or < 2 (NTK: < 4), base <= 1, factor < 1, original <= 0). */
+ST_API st_status_t st_rope_turns(int32_t rot, double base, int32_t scaling, double factor, double original,
+                                 double *turns, float *mscale);
+
+/* Shapes of a norm-and-rotation call.  q and q_out: [batch, heads, n, d]; k and k_out: [batch,
+ * kv_heads, n, d]; in the backward the *_out strides are those of the output gradients, and dq, dk
+ * those of the input gradients.  d: a multiple of 8 up to 256; rot: a multiple of 16, 16 .. d;
+ * dtype: ST_BF16, ST_FP16 or ST_FP32; wdtype: type of wq and wk (dtype or ST_FP32).
+ * positions: int32, element (b, t) at b * pos_batch + t (pos_batch 0: shared by the batch). */
+typedef struct {
+    int64_t batch, heads, kv_heads, n, d, start, pos_batch;
+    int32_t rot, interleaved, dtype, wdtype;
+    float eps, mscale;
+    st_strides_t q, k, q_out, k_out, dq, dk;
+} st_rope_desc_t;
+
+/* Per head row x of q or k: y = x / sqrt(mean(x^2) + eps) * w (wq, wk: [d] weights, or both NULL:
+ * no norm), then the rotation of the first `rot` elements by the angle a_i = 2 pi pos turns[i]:
+ *   half layout (interleaved 0): pairs (i, i + rot/2);  interleaved: pairs (2i, 2i + 1)
+ *   (y0, y1) -> mscale (y0 cos a - y1 sin a, y1 cos a + y0 sin a)
+ * pos = positions[b, t], or start + t when positions is NULL.  Angles are reduced in 64 bits, so far
+ * positions keep their accuracy.  fp32 arithmetic, rounded once.  turns: device fp64 [rot / 2].
+ * q_out may be q and k_out may be k (same strides).  Errors: ST_ERR_INVALID_ARG, ST_ERR_UNSUPPORTED,
+ * ST_ERR_ALIGNMENT, ST_ERR_CUDA. */
+ST_API st_status_t st_qk_norm_rope(const void *q, const void *k, const void *wq, const void *wk,
+                                   const double *turns, const int32_t *positions, void *q_out, void *k_out,
+                                   const st_rope_desc_t *desc, st_stream_t stream);
+
+/* Gradients: gq, gk of the outputs; dq, dk of the inputs (dq may be gq, dk may be gk, same strides);
+ * dwq, dwk: [d] fp32 (NULL without weights), summed in a fixed order. */
+ST_API size_t st_qk_norm_rope_bwd_workspace_bytes(const st_rope_desc_t *desc);
+ST_API st_status_t st_qk_norm_rope_bwd(const void *q, const void *k, const void *gq, const void *gk,
+                                       const void *wq, const void *wk, const double *turns,
+                                       const int32_t *positions, void *dq, void *dk, float *dwq, float *dwk,
+                                       void *workspace, size_t workspace_bytes, const st_rope_desc_t *desc,
+                                       st_stream_t stream);
+
+/* ---- paged key/value cache -------------------------------------------------------------------
+ * Keys and values live in pages of page_size positions: k_pages, v_pages [num_pages, kv_heads,
+ * page_size, d] (strides: batch = page).  A request's block table lists its pages in order; the slot
+ * of a position is page * page_size + its offset. */
+typedef struct {
+    int64_t num_pages, page_size;  /* num_pages * page_size <= 2^31 - 1 */
+    st_strides_t k, v;
+} st_pages_t;
+
+/* One serving step's plan, on the device: block tables and slot maps from the requests' lengths.
+ *   lens, new   [requests] int32: positions already cached, and new tokens of this step
+ *   block_table [requests, max_pages] int32, row stride table_stride: the columns of newly taken
+ *               pages are written, the others left as they were
+ *   free_pages  [*] int32, free_count [1] int32: a stack of free pages; pages are taken from its top,
+ *               free_pages[free_count - 1] first, request by request
+ * Tokens are numbered request by request: request r has tokens offsets[r] .. offsets[r + 1] - 1
+ * (new[r] of them; negative counts as 0).  A request is served unless lens[r] or new[r] is negative,
+ * its positions need more than max_pages pages, its tokens pass `tokens`, or its pages and those
+ * asked for by the requests before it (ones refused for that included) exceed free_count.
+ *   lens_out   [requests]: lens + new of a served request, else lens
+ *   free_left  [1]: free_count less the pages taken
+ *   offsets    [requests + 1]
+ *   slots, positions [tokens]: of each token; -1 for tokens of a request not served and for entries
+ *              past the last token (and the slot of a token whose block table entry is negative)
+ *   status     [requests]: 0 served, 1 not served
+ * Inputs and outputs must not overlap (block_table apart).  requests: 1 .. 16384; tokens: 1 .. 2^30;
+ * page_size: 1 .. 2^20; max_pages: 1 .. 2^24.  Slots are 32-bit: a slot past 2^31 - 1 is given as -1.
+ * Errors: ST_ERR_INVALID_ARG (NULL pointer, sizes, an output that is an input), ST_ERR_UNSUPPORTED
+ * (requests > 16384), ST_ERR_CUDA. */
+typedef struct {
+    int64_t requests, tokens, max_pages, table_stride, page_size, free_capacity;
+} st_plan_desc_t;
+ST_API st_status_t st_paged_plan(const int32_t *lens, const int32_t *new_tokens, int32_t *block_table,
+                                 const int32_t *free_pages, const int32_t *free_count, int32_t *lens_out,
+                                 int32_t *free_left, int32_t *offsets, int32_t *slots, int32_t *positions,
+                                 int32_t *status, const st_plan_desc_t *desc, st_stream_t stream);
+
+/* New tokens into the cache, with their norm and rotation in the same pass: q [tokens, heads, d] ->
+ * q_out, k [tokens, kv_heads, d] -> normed and rotated into its slot of k_pages, v -> v_pages.
+ * desc is as for st_qk_norm_rope with batch = 1 and n = tokens (strides: row = token, head; k_out and
+ * start unused); v: strides of the values.  positions, slots: [tokens] int32, as st_paged_plan gives
+ * them.  A token whose slot is outside 0 .. num_pages * page_size - 1 is skipped: its q_out row and
+ * the cache are left as they were.  Slots must be distinct: of two tokens with one slot either may
+ * be stored, in part. */
+ST_API st_status_t st_paged_append(const void *q, const void *k, const void *v, const void *wq, const void *wk,
+                                   const double *turns, const int32_t *positions, const int32_t *slots,
+                                   void *q_out, void *k_pages, void *v_pages, const st_strides_t *v_strides,
+                                   const st_pages_t *pages, const st_rope_desc_t *desc, st_stream_t stream);
+
+/* Attention of one new token per request over its pages.  q, o: [requests, heads, d] contiguous; lse:
+ * [requests, heads] fp32; block_table as above; lens [requests] int32: keys in the cache, the new
+ * token's included (clamped to 0 .. max_pages * page_size), so the query stands at lens - 1.  A request
+ * of length 0 gets O = 0, lse = -inf.  A key whose page is outside 0 .. num_pages - 1 is not seen, and
+ * the window's error word records it (ST_ERR_BAD_PAGE from st_window_check).  Cache rows that are
+ * not seen are not used, whatever they hold.  d: 64 or 128; dtype: ST_BF16 or ST_FP16; heads / kv_heads
+ * <= 64; page_size a multiple of 16.  The order of the sums depends on lens and on the device
+ * only: the same inputs give the same bits.
+ * Errors: ST_ERR_INVALID_ARG, ST_ERR_UNSUPPORTED, ST_ERR_ALIGNMENT, ST_ERR_NOT_UPLOADED,
+ * ST_ERR_WORKSPACE, ST_ERR_CUDA. */
+typedef struct {
+    int64_t requests, d, max_pages, table_stride;
+    int32_t dtype, reserved;
+    st_pages_t pages;
+} st_paged_desc_t;
+ST_API size_t st_paged_decode_workspace_bytes(const st_paged_desc_t *desc, const st_window_t *window);
+ST_API st_status_t st_paged_decode(const void *q, const void *k_pages, const void *v_pages,
+                                   const int32_t *block_table, const int32_t *lens, const st_window_t *window,
+                                   void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                   const st_paged_desc_t *desc, st_stream_t stream);
 
 /* Static description of a status code. */
 ST_API const char *st_status_string(st_status_t status);
