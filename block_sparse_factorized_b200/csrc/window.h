@@ -80,6 +80,29 @@ struct WindowFwdParams {
     int32_t units, pair_rows;        // pair_rows: a unit is two row tiles of a head, not two heads
 };
 
+struct OutTensor {
+    char *p;
+    int64_t batch, head, row;        // strides in bytes
+};
+
+// Chunks of at most `chunk` steps that a key tile's steps are cut into (one for a tile without any,
+// whose gradients are zero).
+ST_HD int32_t chunks_of(int32_t steps, int32_t chunk) { return steps <= chunk ? 1 : (steps + chunk - 1) / chunk; }
+
+struct WindowBwdParams {
+    CUtensorMap q, k, v, dout;
+    WindowGeom g;
+    RawTensor qraw, kraw, vraw, oraw, doraw;
+    OutTensor dq, dk, dv;
+    const float *lse;
+    float *delta;                    // [batch, heads, nq] D_i (workspace)
+    float *parts;                    // fp32 dV, dK partials of chunked key tiles (workspace)
+    int2 *entries;                   // (key tile, chunk) units, chunked tiles first (workspace)
+    uint32_t *maxima;                // fp16: [batch, kv, 2] largest squared norms of dO and V (workspace)
+    int32_t nentries, nsplit, chunk; // units a key head, those of chunked tiles, steps a chunk at most
+};
+
+cudaError_t launch_window_bwd(const WindowBwdParams &p, int dtype, int d, cudaStream_t s);
 cudaError_t launch_window_fwd(const WindowFwdParams &p, int dtype, int d, cudaStream_t s);
 
 }  // namespace st

@@ -67,6 +67,46 @@ st::WindowGeom geometry(const st_window_desc_t *d, const st_window_t *w, const i
     return g;
 }
 
+// The units of the dK, dV kernel: steps a chunk may have, entries a key head, chunked ones among them.
+struct Units {
+    int32_t chunk, entries, split;
+};
+
+Units plan_units(const st::WindowGeom &g)
+{
+    // A chunk's partial sums cost about five steps' time to write and add (128 KB at d = 128), so
+    // chunks have at least 32; beyond that enough of them for four rounds of the SMs.
+    int64_t total = 0;
+    for (int32_t t = 0; t < g.nkt; ++t) {
+        int32_t i0, i1;
+        st::query_range(g, t, i0, i1);
+        if (i1 >= i0) total += static_cast<int64_t>(i1 - i0 + 1) * g.group;
+    }
+    total *= static_cast<int64_t>(g.batch) * g.kv;
+    const int64_t even = total / (4ll * st::sm_count());
+    Units u{static_cast<int32_t>(even < 32 ? 32 : (even > MAX_POS ? MAX_POS : even)), 0, 0};
+    for (int32_t t = 0; t < g.nkt; ++t) {
+        int32_t i0, i1;
+        st::query_range(g, t, i0, i1);
+        const int32_t c = st::chunks_of(i1 < i0 ? 0 : (i1 - i0 + 1) * g.group, u.chunk);
+        u.entries += c;
+        if (c > 1) u.split += c;
+    }
+    return u;
+}
+
+struct BwdSizes {
+    size_t delta, entries, parts, maxima;
+    size_t total() const { return delta + entries + parts + maxima; }
+};
+
+BwdSizes bwd_sizes(const st::WindowGeom &g, const Units &u, int64_t d)
+{
+    const size_t bk = static_cast<size_t>(g.batch) * g.kv;
+    return {st::round256(static_cast<size_t>(g.batch) * g.heads * g.nq * sizeof(float)), st::round256(u.entries * sizeof(int2)),
+            bk * u.split * 2 * 128 * d * sizeof(float), st::round256(bk * 2 * sizeof(uint32_t))};
+}
+
 }  // namespace
 
 extern "C" {
@@ -103,12 +143,61 @@ st_status_t st_window_fwd(const void *q, const void *k, const void *v, const int
     return st::launch_window_fwd(p, desc->dtype, static_cast<int>(desc->d), stream) == cudaSuccess ? ST_OK : ST_ERR_CUDA;
 }
 
-}  // extern "C"
-extern "C" {
-size_t st_window_bwd_workspace_bytes(const st_window_desc_t *, const st_window_t *) { return 0; }
-st_status_t st_window_bwd(const void *, const void *, const void *, const void *, const float *, const void *, const int32_t *,
-                          const st_window_t *, void *, void *, void *, void *, size_t, const st_window_desc_t *, st_stream_t)
+size_t st_window_bwd_workspace_bytes(const st_window_desc_t *desc, const st_window_t *w)
 {
-    return ST_ERR_UNSUPPORTED;
+    if (check_sizes(desc, w) != ST_OK) return 0;
+    const st::WindowGeom g = geometry(desc, w, nullptr);
+    return bwd_sizes(g, plan_units(g), desc->d).total();
 }
+
+st_status_t st_window_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *dO,
+                          const int32_t *lens, const st_window_t *w, void *dq, void *dk, void *dv, void *workspace,
+                          size_t workspace_bytes, const st_window_desc_t *desc, st_stream_t stream)
+{
+    if (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv) return ST_ERR_INVALID_ARG;
+    st_status_t cs = check_sizes(desc, w);
+    if (cs != ST_OK) return cs;
+    const st_strides_t *qs[] = {&desc->q, &desc->o, &desc->dout, &desc->dq}, *ks[] = {&desc->k, &desc->v, &desc->dk, &desc->dv};
+    for (int i = 0; i < 4; ++i)
+        if ((cs = check_strides(*qs[i], desc->batch, w->heads, desc->nq, desc->d, 2)) != ST_OK ||
+            (cs = check_strides(*ks[i], desc->batch, w->kv_heads, desc->nk, desc->d, 2)) != ST_OK)
+            return cs;
+    for (const void *p : {q, k, v, o, dO, static_cast<const void *>(dq), static_cast<const void *>(dk), static_cast<const void *>(dv)})
+        if (!aligned_to(p, 16)) return ST_ERR_ALIGNMENT;
+    if (!aligned_to(lse, 4) || !aligned_to(lens, 4)) return ST_ERR_ALIGNMENT;
+    if ((cs = st::check_window(w)) != ST_OK) return cs;
+    st::WindowBwdParams p;
+    memset(&p, 0, sizeof(p));
+    p.g = geometry(desc, w, lens);
+    const Units u = plan_units(p.g);
+    const BwdSizes z = bwd_sizes(p.g, u, desc->d);
+    if (static_cast<int64_t>(u.entries) * p.g.batch * p.g.kv > INT32_MAX ||
+        static_cast<int64_t>(u.split) * p.g.batch * p.g.kv * 2 > INT32_MAX)
+        return ST_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < z.total()) return ST_ERR_WORKSPACE;
+    if (!aligned_to(workspace, 256)) return ST_ERR_ALIGNMENT;
+    if (!st::encode_fn()) return ST_ERR_CUDA;
+    if (!make_map(&p.q, q, desc->q, desc, w->heads, desc->nq) || !make_map(&p.k, k, desc->k, desc, w->kv_heads, desc->nk) ||
+        !make_map(&p.v, v, desc->v, desc, w->kv_heads, desc->nk) || !make_map(&p.dout, dO, desc->dout, desc, w->heads, desc->nq))
+        return ST_ERR_CUDA;
+    p.qraw = raw(q, desc->q);
+    p.kraw = raw(k, desc->k);
+    p.vraw = raw(v, desc->v);
+    p.oraw = raw(o, desc->o);
+    p.doraw = raw(dO, desc->dout);
+    p.dq = {static_cast<char *>(dq), desc->dq.batch * 2, desc->dq.head * 2, desc->dq.row * 2};
+    p.dk = {static_cast<char *>(dk), desc->dk.batch * 2, desc->dk.head * 2, desc->dk.row * 2};
+    p.dv = {static_cast<char *>(dv), desc->dv.batch * 2, desc->dv.head * 2, desc->dv.row * 2};
+    p.lse = lse;
+    char *ws = static_cast<char *>(workspace);
+    p.delta = reinterpret_cast<float *>(ws);
+    p.entries = reinterpret_cast<int2 *>(ws + z.delta);
+    p.parts = reinterpret_cast<float *>(ws + z.delta + z.entries);
+    p.maxima = reinterpret_cast<uint32_t *>(ws + z.delta + z.entries + z.parts);
+    p.nentries = u.entries;
+    p.nsplit = u.split;
+    p.chunk = u.chunk;
+    return st::launch_window_bwd(p, desc->dtype, static_cast<int>(desc->d), stream) == cudaSuccess ? ST_OK : ST_ERR_CUDA;
 }
+
+}  // extern "C"
