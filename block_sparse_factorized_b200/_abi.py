@@ -150,7 +150,7 @@ def load() -> ctypes.CDLL:
     lib.st_window_bwd_workspace_bytes.argtypes = [pp(st_window_desc_t), P]
     lib.st_window_bwd_workspace_bytes.restype = sz
     lib.st_window_bwd.argtypes = [P] * 12 + [sz, pp(st_window_desc_t), P]
-    lib.st_rope_turns.argtypes = [i32, f64, i32, f64, f64, pp(f64), pp(ctypes.c_float)]
+    lib.st_rope_turns.argtypes = [i32, f64, i32, f64, f64, P, pp(ctypes.c_float)]
     lib.st_qk_norm_rope.argtypes = [P] * 8 + [pp(st_rope_desc_t), P]
     lib.st_qk_norm_rope_bwd_workspace_bytes.argtypes = [pp(st_rope_desc_t)]
     lib.st_qk_norm_rope_bwd_workspace_bytes.restype = sz

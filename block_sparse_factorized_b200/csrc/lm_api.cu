@@ -33,13 +33,14 @@ st_status_t check_rope(const st_rope_desc_t *d)
         !known_dtype(d->dtype) || (d->wdtype != d->dtype && d->wdtype != ST_FP32) || !(d->eps >= 0.f) ||
         d->rot < 1 || d->rot > d->d || (d->interleaved != 0 && d->interleaved != 1))
         return ST_ERR_INVALID_ARG;
-    if (d->d > 256 || d->d % 8 != 0 || d->rot % 16 != 0 || d->batch > MAX_POS || d->n > MAX_POS ||
-        d->batch * d->n > MAX_POS || d->heads > 4096 || d->kv_heads > 4096)
+    if (d->d > 256 || d->d % 16 != 0 || d->rot % 16 != 0 || d->batch > MAX_POS || d->n > MAX_POS ||
+        d->batch * d->n > MAX_POS || d->heads > 4096 || d->kv_heads > 4096 ||
+        d->batch * d->n * ((d->heads + 2 * d->kv_heads + 1) / 2) > INT32_MAX)
         return ST_ERR_UNSUPPORTED;
     return ST_OK;
 }
 
-st::RopeParams rope_params(const st_rope_desc_t *d, const void *wq, const void *wk, const double *turns,
+st::RopeParams rope_params(const st_rope_desc_t *d, const void *wq, const void *wk, const uint64_t *turns,
                            const int32_t *positions)
 {
     st::RopeParams p;
@@ -144,29 +145,30 @@ void st_window_destroy(st_window_t *w)
 
 // ---- norm and rotation --------------------------------------------------------------------------
 
-st_status_t st_rope_turns(int32_t rot, double base, int32_t scaling, double factor, double original, double *turns,
+st_status_t st_rope_turns(int32_t rot, double base, int32_t scaling, double factor, double original, uint64_t *turns,
                           float *mscale)
 {
     if (!turns || !mscale || rot < 2 || rot % 2 != 0 || !(base > 1.0) || !isfinite(base) || !(factor >= 1.0) ||
         !isfinite(factor) || scaling < ST_ROPE_NONE || scaling > ST_ROPE_YARN ||
         (scaling == ST_ROPE_YARN && !(original > 0.0 && isfinite(original))) || (scaling == ST_ROPE_NTK && rot < 4))
         return ST_ERR_INVALID_ARG;
-    const double two_pi = 6.283185307179586476925286766559;
-    if (scaling == ST_ROPE_NTK) base *= pow(factor, static_cast<double>(rot) / (rot - 2));
+    const long double two_pi = 6.283185307179586476925286766559L;
+    long double theta = base;
+    if (scaling == ST_ROPE_NTK) theta *= powl(factor, static_cast<long double>(rot) / (rot - 2));
     for (int32_t i = 0; i < rot / 2; ++i) {
-        double w = pow(base, -2.0 * i / rot);
+        long double w = powl(theta, -2.0L * i / rot);
         if (scaling == ST_ROPE_LINEAR) w /= factor;
         if (scaling == ST_ROPE_YARN) {
-            const double t = fmin(1.0, fmax(0.0, (original * w / two_pi - 1.0) / 31.0));
-            w *= t + (1.0 - t) / factor;
+            const long double t = fminl(1.0L, fmaxl(0.0L, (original * w / two_pi - 1.0L) / 31.0L));
+            w *= t + (1.0L - t) / factor;
         }
-        turns[i] = w / two_pi;
+        turns[i] = static_cast<uint64_t>(w / two_pi * 0x1p64L + 0.5L);  // w <= 1: under 2^62
     }
     *mscale = scaling == ST_ROPE_YARN ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.0f;
     return ST_OK;
 }
 
-st_status_t st_qk_norm_rope(const void *q, const void *k, const void *wq, const void *wk, const double *turns,
+st_status_t st_qk_norm_rope(const void *q, const void *k, const void *wq, const void *wk, const uint64_t *turns,
                             const int32_t *positions, void *q_out, void *k_out, const st_rope_desc_t *desc,
                             st_stream_t stream)
 {
@@ -190,12 +192,13 @@ st_status_t st_qk_norm_rope(const void *q, const void *k, const void *wq, const 
 size_t st_qk_norm_rope_bwd_workspace_bytes(const st_rope_desc_t *desc)
 {
     if (check_rope(desc) != ST_OK) return 0;
-    const int64_t tile = st::rope_tile(desc->batch * desc->n), tiles = (desc->n + tile - 1) / tile;
-    return round256(static_cast<size_t>(st::rope_bwd_ctas(desc->batch * tiles)) * 2 * desc->d * sizeof(float));
+    const st::RopeCtas c = st::rope_bwd_ctas(desc->batch * desc->n, static_cast<int>(desc->heads),
+                                             static_cast<int>(desc->kv_heads), static_cast<int>(desc->d));
+    return round256(static_cast<size_t>(c.q + c.k) * desc->d * sizeof(float));
 }
 
 st_status_t st_qk_norm_rope_bwd(const void *q, const void *k, const void *gq, const void *gk, const void *wq,
-                                const void *wk, const double *turns, const int32_t *positions, void *dq, void *dk,
+                                const void *wk, const uint64_t *turns, const int32_t *positions, void *dq, void *dk,
                                 float *dwq, float *dwk, void *workspace, size_t workspace_bytes,
                                 const st_rope_desc_t *desc, st_stream_t stream)
 {
@@ -261,7 +264,7 @@ st_status_t st_paged_plan(const int32_t *lens, const int32_t *new_tokens, int32_
 }
 
 st_status_t st_paged_append(const void *q, const void *k, const void *v, const void *wq, const void *wk,
-                            const double *turns, const int32_t *positions, const int32_t *slots, void *q_out,
+                            const uint64_t *turns, const int32_t *positions, const int32_t *slots, void *q_out,
                             void *k_pages, void *v_pages, const st_strides_t *v_strides, const st_pages_t *pages,
                             const st_rope_desc_t *desc, st_stream_t stream)
 {

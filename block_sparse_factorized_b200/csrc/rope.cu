@@ -8,11 +8,15 @@
 // m (g1 cos a - g0 sin a)); with u = r x,  dw = sum g' u  and  dx = r (g' w - u mean(g' w u)).
 //
 // Bound by memory: two passes over the rows (three for the gradient) and about 3 operations per
-// byte, so each row is read once, kept in registers (8 elements a lane, 4 to 32 lanes a row) and
-// written once.  cos and sin are shared by all heads of a token: a CTA takes a few tokens, puts
-// their (cos, sin) pairs into shared memory once and then works through the heads.  The angle is
-// p turns[i] in 64 bits less its nearest whole number, exact to 2^-25 turns wherever p stands; a
-// table of cosines would have to be read for every position instead.
+// byte, so each row is read once, kept in registers and written once, and the instructions a row costs
+// decide: at 130 a row and warp the kernel was bound by issue at a third of the memory's rate.  So a
+// lane holds 16 elements, both of each of its eight pairs (in the half layout two pieces of 8, rot / 2
+// apart), and the rotation needs no exchange; a group of 2 to 16 lanes takes one token and a run of
+// its heads, whose cosines and sines stay in registers; and a run's last rows are repeated rather than
+// predicated.  The angle is p turns[i] modulo a turn, with turns[i] in units of 2^-64 turns and the
+// product in 64-bit integers: exact to 2^-25 turns wherever p stands, and a few integer instructions (in
+// fp64 the conversions alone took a fifth of the kernel's time); a table of cosines would have to be
+// read for every position instead.
 #include "elem.cuh"
 #include "kernels.h"
 #include "lm.h"
@@ -22,275 +26,296 @@ namespace st {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int MAX_TOKENS = 8;  // tokens a CTA takes at a time
-constexpr int MAX_PAIRS = 128;
+constexpr int U = 4;  // rows a group has in flight
 
-struct Work {
-    const RopeParams &p;
-    int l, grp;       // lane in the row's group, group in the CTA
-    bool active;      // the lane holds elements of the row (d / 8 need not be a power of two)
-    bool turns;       // the lane's elements are rotated
-    int pair0, src;   // first pair of the lane's elements; the lane with the partners (half layout)
-    bool second;      // half layout: the lane holds the second elements of its pairs
+// The lane's part in its group's rows: elements a .. a + 7 and b .. b + 7.
+template <int L>
+struct Lane {
+    int l, grp, a, b;
+    uint32_t mask;    // the group's lanes of the warp
+    bool active;      // d / 16 need not be a power of two
+    bool turns;       // the elements are rotated: eight pairs, the first being pair 8 l
+    bool inter;       // pairs (a, a + 1), (a + 2, a + 3), ..; else (a + i, b + i)
 
-    template <int L>
-    __device__ static Work make(const RopeParams &p)
+    __device__ explicit Lane(const RopeParams &p)
     {
-        const int l = threadIdx.x % L, e0 = 8 * l, half = p.rot / 2;
-        Work w{p, l, static_cast<int>(threadIdx.x) / L, e0 < p.d, e0 < p.rot, 0, l, false};
-        if (p.interleaved) {
-            w.pair0 = e0 / 2;
-        } else {
-            w.second = e0 >= half;
-            w.pair0 = w.second ? e0 - half : e0;
-            if (w.turns) w.src = w.second ? l - half / 8 : l + half / 8;
-        }
-        return w;
+        l = threadIdx.x % L;
+        grp = threadIdx.x / L;
+        mask = ((1u << L) - 1u) << ((threadIdx.x & 31) / L * L);
+        active = 16 * l < p.d;
+        turns = 16 * l < p.rot;
+        inter = p.interleaved != 0;
+        a = turns && !inter ? 8 * l : (active ? 16 * l : 0);  // (an idle lane reads lane 0's place)
+        b = turns && !inter ? p.rot / 2 + 8 * l : a + 8;
+    }
+    __device__ float sum(float x) const
+    {
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(mask, x, o);
+        return x;
     }
 };
 
-template <int L>
-__device__ __forceinline__ float group_sum(float x)
+// cos and sin (times mscale) of the lane's pairs.  For 16-bit rows the fast forms do: their error of some
+// 2^-21 is far below the rounding of the result (2^-12 and 2^-9).
+template <int DT, int L>
+__device__ __forceinline__ void angles(const RopeParams &p, const Lane<L> &w, int64_t pos, float (&c)[8], float (&s)[8])
 {
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-
-// The rotation (dir = 1) or its transpose (dir = -1) of the lane's 8 elements.  Every lane of the
-// warp takes part in the exchange.
-template <int L>
-__device__ __forceinline__ void rotate(const Work &w, const float2 *cs, float dir, float (&x)[8])
-{
-    if (w.p.interleaved) {
-        if (!w.turns) return;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 t = cs[w.pair0 + e];
-            const float s = dir * t.y, a = x[2 * e], b = x[2 * e + 1];
-            x[2 * e] = a * t.x - b * s;
-            x[2 * e + 1] = b * t.x + a * s;
-        }
-        return;
-    }
-    const float sign = w.second ? dir : -dir;
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = __shfl_sync(0xffffffffu, x[e], w.src, L);
-    if (!w.turns) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float2 t = cs[w.pair0 + e];
-        x[e] = x[e] * t.x + sign * t.y * y[e];
+        const uint64_t a = w.turns ? static_cast<uint64_t>(pos) * p.turns[8 * w.l + e] : 0ull;
+        const float half_turns = static_cast<float>(static_cast<int32_t>(a >> 32)) * 0x1p-31f;  // -1 .. 1
+        if constexpr (DT == ST_FP32)
+            sincospif(half_turns, &s[e], &c[e]);
+        else
+            __sincosf(half_turns * 3.14159265f, &s[e], &c[e]);
+        c[e] *= p.mscale;
+        s[e] *= p.mscale;
     }
 }
 
-// (cos, sin) times mscale of the tile's tokens t0 .. t0 + nt - 1 of batch element b.
-__device__ __forceinline__ void fill_angles(const RopeParams &p, int64_t b, int64_t t0, int nt, float2 *cs)
+// The rotation (of the transpose: s negated) of the lane's elements x[0 .. 7] = a .., x[8 .. 15] = b ..
+template <int L>
+__device__ __forceinline__ void rotate(const Lane<L> &w, const float (&c)[8], const float (&s)[8], float (&x)[16])
 {
-    const int half = p.rot / 2;
-    for (int i = threadIdx.x; i < nt * half; i += THREADS) {
-        const int tk = i / half, k = i - tk * half;
-        const int64_t t = t0 + tk;
-        const double pos = p.positions ? static_cast<double>(p.positions[b * p.pos_batch + t])
-                                       : static_cast<double>(p.start + t);
-        double a = pos * p.turns[k];
-        a -= rint(a);
-        float s, c;
-        sincospif(2.f * static_cast<float>(a), &s, &c);
-        cs[i] = make_float2(c * p.mscale, s * p.mscale);
+    if (!w.turns) return;
+    if (w.inter) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float u = x[2 * e], v = x[2 * e + 1];
+            x[2 * e] = u * c[e] - v * s[e];
+            x[2 * e + 1] = v * c[e] + u * s[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float u = x[e], v = x[e + 8];
+            x[e] = u * c[e] - v * s[e];
+            x[e + 8] = v * c[e] + u * s[e];
+        }
     }
+}
+
+// The lane's two pieces of a row, as loaded.
+template <int DT>
+struct Row {
+    Vec8<DT> a, b;
+};
+
+template <int DT>
+__device__ __forceinline__ Row<DT> load_row(const char *row, int a, int b)
+{
+    constexpr int ES = DT == ST_FP32 ? 4 : 2;
+    return {load8<DT>(row + ES * a), load8<DT>(row + ES * b)};
 }
 
 template <int DT>
-__device__ __forceinline__ void load_weights(const RopeParams &p, const void *w, const Work &k, float (&x)[8])
+__device__ __forceinline__ void store_row(char *row, int a, int b, const Row<DT> &v)
 {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    if (!w || !k.active) return;
-    if (p.w_f32)
-        widen8<ST_FP32>(load8<ST_FP32>(static_cast<const float *>(w) + 8 * k.l), x);
-    else
-        widen8<DT>(load8<DT>(static_cast<const char *>(w) + 8 * k.l * (DT == ST_FP32 ? 4 : 2)), x);
+    constexpr int ES = DT == ST_FP32 ? 4 : 2;
+    store8<DT>(row + ES * a, v.a);
+    store8<DT>(row + ES * b, v.b);
 }
 
-__device__ __forceinline__ char *row_at(const RopeTensor &t, int64_t b, int64_t h, int64_t r)
+template <int DT>
+__device__ __forceinline__ void widen(const Row<DT> &v, float (&x)[16])
 {
-    return t.p + b * t.batch + h * t.head + r * t.row;
+    widen8<DT>(v.a, *reinterpret_cast<float(*)[8]>(&x[0]));
+    widen8<DT>(v.b, *reinterpret_cast<float(*)[8]>(&x[8]));
 }
 
-constexpr int UNROLL = 4;  // rows a group has in flight
-
-// Head row j of a token: 0 .. heads - 1 queries, then the keys, then (append) the values.
-template <int DT, int L, bool APPEND>
-__global__ void __launch_bounds__(THREADS) rope_fwd_kernel(const __grid_constant__ RopeParams p)
+template <int DT>
+__device__ __forceinline__ Row<DT> narrow(const float (&x)[16])
 {
-    constexpr int ES = DT == ST_FP32 ? 4 : 2, NG = THREADS / L;
-    __shared__ float2 cs[MAX_TOKENS * MAX_PAIRS];
-    const int64_t b = blockIdx.x / p.tiles, t0 = (blockIdx.x - b * p.tiles) * static_cast<int64_t>(p.tile);
-    const int nt = static_cast<int>(min(static_cast<int64_t>(p.tile), p.n - t0));
-    const Work w = Work::make<L>(p);
-    float wq[8], wk[8];
-    load_weights<DT>(p, p.wq, w, wq);
-    load_weights<DT>(p, p.wk, w, wk);
-    fill_angles(p, b, t0, nt, cs);
-    __syncthreads();
-    const int nh = p.heads + p.kv + (APPEND ? p.kv : 0), rows = nt * nh;
-    for (int r0 = 0; r0 < rows; r0 += UNROLL * NG) {
-        Vec8<DT> v[UNROLL];
-        char *dst[UNROLL];
-        int tk[UNROLL], j[UNROLL];
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int r = r0 + u * NG + w.grp;
-            dst[u] = nullptr;
-            tk[u] = r / nh;
-            j[u] = r - tk[u] * nh;
-#pragma unroll
-            for (auto &q : v[u].r) q = make_uint4(0u, 0u, 0u, 0u);
-            if (r >= rows) {
-                tk[u] = 0;
-                continue;
-            }
-            const int64_t t = t0 + tk[u];
-            const bool isq = j[u] < p.heads, isk = !isq && j[u] < p.heads + p.kv;
-            const int h = isq ? j[u] : (isk ? j[u] - p.heads : j[u] - p.heads - p.kv);
-            if constexpr (APPEND) {
-                const int64_t slot = p.slots[t];
-                if (slot < 0 || slot >= p.nslots) continue;
-                const int64_t page = slot / p.page_size, at = slot - page * p.page_size;
-                dst[u] = isq ? row_at(p.qo, 0, h, t) : row_at(isk ? p.ko : p.vo, page, h, at);
-            } else {
-                dst[u] = row_at(isq ? p.qo : p.ko, b, h, t);
-            }
-            if (w.active) v[u] = load8<DT>(row_at(isq ? p.q : (isk ? p.k : p.v), b, h, t) + 8 * w.l * ES);
-        }
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const bool copy = APPEND && j[u] >= p.heads + p.kv;  // a value row
-            float x[8];
-            widen8<DT>(v[u], x);
-            if (p.wq) {
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-                const float r = rsqrtf(group_sum<L>(ss) * p.inv_d + p.eps);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = x[e] * r * (j[u] < p.heads ? wq[e] : wk[e]);
-            }
-            rotate<L>(w, cs + tk[u] * (p.rot / 2), 1.f, x);
-            if (dst[u] && w.active) store8<DT>(dst[u] + 8 * w.l * ES, copy ? v[u] : round8<DT>(x));
-        }
-    }
+    return {round8<DT>(*reinterpret_cast<const float(*)[8]>(&x[0])), round8<DT>(*reinterpret_cast<const float(*)[8]>(&x[8]))};
 }
 
-// One CTA walks tiles blockIdx.x, blockIdx.x + gridDim.x, ...: the weights' gradients stay in its
-// registers and leave as one partial row a CTA, added in a fixed order by rope_dw_kernel.
 template <int DT, int L>
-__global__ void __launch_bounds__(THREADS) rope_bwd_kernel(const __grid_constant__ RopeParams p)
+__device__ __forceinline__ void load_weights(const RopeParams &p, const void *w, const Lane<L> &k, float (&x)[16])
 {
-    constexpr int ES = DT == ST_FP32 ? 4 : 2, NG = THREADS / L, U = 2;
-    __shared__ float2 cs[MAX_TOKENS * MAX_PAIRS];
-    __shared__ float red[NG][8 * L];
-    const Work w = Work::make<L>(p);
-    float wq[8], wk[8], aq[8], ak[8];
-    load_weights<DT>(p, p.wq, w, wq);
-    load_weights<DT>(p, p.wk, w, wk);
+    if (!w) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) aq[e] = ak[e] = 0.f;
-    const int nh = p.heads + p.kv;
-    for (int64_t tile = blockIdx.x; tile < static_cast<int64_t>(p.batch) * p.tiles; tile += gridDim.x) {
-        const int64_t b = tile / p.tiles, t0 = (tile - b * p.tiles) * p.tile;
-        const int nt = static_cast<int>(min(static_cast<int64_t>(p.tile), p.n - t0)), rows = nt * nh;
-        __syncthreads();  // the previous tile's angles are no longer read
-        fill_angles(p, b, t0, nt, cs);
-        __syncthreads();
-        for (int r0 = 0; r0 < rows; r0 += U * NG) {
-            Vec8<DT> vx[U], vg[U];
-            char *dst[U];
-            int tk[U], j[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = r0 + u * NG + w.grp;
-                tk[u] = r / nh;
-                j[u] = r - tk[u] * nh;
-                dst[u] = nullptr;
-#pragma unroll
-                for (auto &q : vx[u].r) q = make_uint4(0u, 0u, 0u, 0u);
-                vg[u] = vx[u];
-                if (r >= rows) {
-                    tk[u] = 0;
-                    continue;
-                }
-                const bool isq = j[u] < p.heads;
-                const int h = isq ? j[u] : j[u] - p.heads;
-                const int64_t t = t0 + tk[u];
-                dst[u] = row_at(isq ? p.qo : p.ko, b, h, t);
-                if (w.active) {
-                    if (p.wq) vx[u] = load8<DT>(row_at(isq ? p.q : p.k, b, h, t) + 8 * w.l * ES);
-                    vg[u] = load8<DT>(row_at(isq ? p.gq : p.gk, b, h, t) + 8 * w.l * ES);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float g[8];
-                widen8<DT>(vg[u], g);
-                rotate<L>(w, cs + tk[u] * (p.rot / 2), -1.f, g);
-                if (p.wq) {
-                    const bool isq = j[u] < p.heads;
-                    float x[8], ss = 0.f, dot = 0.f;
-                    widen8<DT>(vx[u], x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-                    const float r = rsqrtf(group_sum<L>(ss) * p.inv_d + p.eps);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[e] *= r;
-                        const float t = g[e] * x[e];
-                        aq[e] += isq ? t : 0.f;  // rows past the tile were loaded as zeros
-                        ak[e] += isq ? 0.f : t;
-                        g[e] *= isq ? wq[e] : wk[e];
-                        dot = fmaf(g[e], x[e], dot);
-                    }
-                    dot = group_sum<L>(dot) * p.inv_d;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) g[e] = r * (g[e] - x[e] * dot);
-                }
-                if (dst[u] && w.active) store8<DT>(dst[u] + 8 * w.l * ES, round8<DT>(g));
-            }
-        }
-    }
-    if (!p.wq) return;
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) red[w.grp][8 * w.l + e] = which ? ak[e] : aq[e];
-        __syncthreads();
-        for (int c = threadIdx.x; c < p.d; c += THREADS) {
-            float s = 0.f;
-#pragma unroll
-            for (int gi = 0; gi < NG; ++gi) s += red[gi][c];
-            p.partial[(static_cast<size_t>(blockIdx.x) * 2 + which) * p.d + c] = s;
-        }
+        for (int e = 0; e < 16; ++e) x[e] = 1.f;
+    } else if (p.w_f32) {
+        widen<ST_FP32>(load_row<ST_FP32>(static_cast<const char *>(w), k.a, k.b), x);
+    } else {
+        widen<DT>(load_row<DT>(static_cast<const char *>(w), k.a, k.b), x);
     }
 }
 
-// dw = sum of the CTAs' partial rows: 32 columns by 32 row lanes a CTA, the lanes added in order.
-__global__ void __launch_bounds__(1024) rope_dw_kernel(const float *partial, int32_t rows, int32_t d, float *dwq, float *dwk)
+// A group's item: a token (b, t) and the rows j0 .. j1 - 1 of its heads (queries, then keys, then for
+// an append values).
+struct Item {
+    int64_t b, t;
+    int j0, j1;
+};
+
+__device__ __forceinline__ Item item_of(const RopeParams &p, uint32_t i, int nh, int run, int parts)
+{
+    Item r;
+    const uint32_t token = i / static_cast<uint32_t>(parts), part = i - token * parts;
+    r.b = token / static_cast<uint32_t>(p.n);
+    r.t = token - static_cast<uint32_t>(r.b) * static_cast<uint32_t>(p.n);
+    r.j0 = static_cast<int>(part) * run;
+    r.j1 = min(nh, r.j0 + run);
+    return r;
+}
+
+__device__ __forceinline__ int64_t position(const RopeParams &p, const Item &it)
+{
+    return p.positions ? p.positions[it.b * p.pos_batch + it.t] : p.start + it.t;
+}
+
+template <int DT, int L, bool APPEND>
+__global__ void __launch_bounds__(THREADS, DT == ST_FP32 ? 1 : 2) rope_fwd_kernel(const __grid_constant__ RopeParams p)
+{
+    constexpr int NG = THREADS / L;
+    const Lane<L> w(p);
+    const uint32_t i = blockIdx.x * NG + w.grp;
+    if (i >= p.items) return;
+    const Item it = item_of(p, i, p.heads + p.kv + (APPEND ? p.kv : 0), p.run, p.parts);
+    int64_t page = 0, at = 0;
+    if constexpr (APPEND) {
+        const int32_t slot = p.slots[it.t];
+        if (slot < 0 || slot >= p.nslots) return;
+        page = static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.page_size);
+        at = slot - page * p.page_size;
+    }
+    float c[8], s[8];
+    angles<DT>(p, w, position(p, it), c, s);
+    const bool norm = p.wq != nullptr;
+    // rows lo .. hi - 1 of a token's heads from src (head 0) to dst, U at a time; the last are repeated
+    auto part = [&](int lo, int hi, const char *src, int64_t src_head, char *dst, int64_t dst_head, const void *weights, bool copy) {
+        const int first = max(it.j0, lo), n = min(it.j1, hi) - first;
+        if (n <= 0) return;
+        float wt[16];
+        load_weights<DT>(p, weights, w, wt);
+        src += (first - lo) * src_head;
+        dst += (first - lo) * dst_head;
+        for (int j = 0; j < n; j += U) {
+            Row<DT> v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = load_row<DT>(src + min(j + u, n - 1) * src_head, w.a, w.b);
+            if (!copy) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float x[16];
+                    widen<DT>(v[u], x);
+                    if (norm) {
+                        float ss = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+                        const float r = rsqrtf(w.sum(w.active ? ss : 0.f) * p.inv_d + p.eps);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) x[e] *= r * wt[e];
+                    }
+                    rotate(w, c, s, x);
+                    v[u] = narrow<DT>(x);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (w.active) store_row<DT>(dst + min(j + u, n - 1) * dst_head, w.a, w.b, v[u]);
+        }
+    };
+    auto row = [&](const RopeTensor &t) { return t.p + it.b * t.batch + it.t * t.row; };
+    part(0, p.heads, row(p.q), p.q.head, row(p.qo), p.qo.head, p.wq, false);
+    if constexpr (APPEND) {
+        part(p.heads, p.heads + p.kv, row(p.k), p.k.head, p.ko.p + page * p.ko.batch + at * p.ko.row, p.ko.head, p.wk, false);
+        part(p.heads + p.kv, p.heads + 2 * p.kv, row(p.v), p.v.head, p.vo.p + page * p.vo.batch + at * p.vo.row, p.vo.head, nullptr, true);
+    } else {
+        part(p.heads, p.heads + p.kv, row(p.k), p.k.head, row(p.ko), p.ko.head, p.wk, false);
+    }
+}
+
+// The first q_ctas CTAs take the queries, the others the keys; a group walks its tokens and keeps the
+// weights and their gradient in its registers, which leave as one partial row a CTA, added in a fixed
+// order by rope_dw_kernel.
+template <int DT, int L>
+__global__ void __launch_bounds__(THREADS, DT == ST_FP32 ? 1 : 2) rope_bwd_kernel(const __grid_constant__ RopeParams p)
+{
+    constexpr int NG = THREADS / L;
+    __shared__ float red[NG][16 * L];
+    const Lane<L> w(p);
+    const bool norm = p.wq != nullptr, isq = blockIdx.x < static_cast<unsigned>(p.q_ctas);
+    const RopeTensor &xs = isq ? p.q : p.k, &gs = isq ? p.gq : p.gk, &ds = isq ? p.qo : p.ko;
+    const uint32_t cta = isq ? blockIdx.x : blockIdx.x - p.q_ctas, ctas = isq ? p.q_ctas : gridDim.x - p.q_ctas;
+    const int rows = isq ? p.heads : p.kv, run = isq ? p.run : p.run_k, parts = isq ? p.parts : p.parts_k;
+    const uint32_t items = isq ? p.items : p.items_k;
+    float wt[16], acc[16];
+    load_weights<DT>(p, isq ? p.wq : p.wk, w, wt);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+    for (uint32_t i = cta * NG + w.grp; i < items; i += ctas * NG) {
+        const Item it = item_of(p, i, rows, run, parts);
+        const int n = it.j1 - it.j0;
+        const char *xp = xs.p + it.b * xs.batch + it.t * xs.row + it.j0 * xs.head;
+        const char *gp = gs.p + it.b * gs.batch + it.t * gs.row + it.j0 * gs.head;
+        char *dp = ds.p + it.b * ds.batch + it.t * ds.row + it.j0 * ds.head;
+        Row<DT> ng = load_row<DT>(gp, w.a, w.b), nx = ng;  // the next row, on its way
+        if (norm) nx = load_row<DT>(xp, w.a, w.b);
+        float c[8], s[8];
+        angles<DT>(p, w, position(p, it), c, s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = -s[e];  // the transpose
+        for (int j = 0; j < n; ++j) {
+            const Row<DT> vg = ng, vx = nx;
+            if (j + 1 < n) {
+                ng = load_row<DT>(gp + (j + 1) * gs.head, w.a, w.b);
+                if (norm) nx = load_row<DT>(xp + (j + 1) * xs.head, w.a, w.b);
+            }
+            float g[16];
+            widen<DT>(vg, g);
+            rotate(w, c, s, g);
+            if (norm) {  // with t = r g' x: dw += t, dx = r w g' - x r^2 mean(w t)
+                float x[16], ss = 0.f, dot = 0.f;
+                widen<DT>(vx, x);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+                const float r = rsqrtf(w.sum(w.active ? ss : 0.f) * p.inv_d + p.eps);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float t = g[e] * (x[e] * r);
+                    acc[e] += t;
+                    dot = fmaf(t, wt[e], dot);
+                }
+                const float k = -(w.sum(w.active ? dot : 0.f) * p.inv_d) * r * r;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) g[e] = fmaf(x[e], k, g[e] * (wt[e] * r));
+            }
+            if (w.active) store_row<DT>(dp + j * ds.head, w.a, w.b, narrow<DT>(g));
+        }
+    }
+    if (!norm) return;
+    if (w.active) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) red[w.grp][e < 8 ? w.a + e : w.b + e - 8] = acc[e];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.d; c += THREADS) {
+        float t = 0.f;
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) t += red[gi][c];
+        p.partial[static_cast<size_t>(blockIdx.x) * p.d + c] = t;
+    }
+}
+
+// dw = sum of the CTAs' partial rows (rows 0 .. q_rows - 1: the queries', the others the keys'): 32
+// columns by 32 row lanes a CTA, the lanes added in order.
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float *partial, int32_t q_rows, int32_t rows, int32_t d, float *dwq, float *dwk)
 {
     __shared__ float red[32][33];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5, lo = blockIdx.y ? q_rows : 0, hi = blockIdx.y ? rows : q_rows;
     float s = 0.f;
-    if (c < 2 * d)
+    if (c < d)
 #pragma unroll 8
-        for (int r = lane; r < rows; r += 32) s += partial[static_cast<size_t>(r) * 2 * d + c];
+        for (int r = lo + lane; r < hi; r += 32) s += partial[static_cast<size_t>(r) * d + c];
     red[lane][threadIdx.x & 31] = s;
     __syncthreads();
-    if (lane == 0 && c < 2 * d) {
+    if (lane == 0 && c < d) {
         s = 0.f;
         for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
-        (c < d ? dwq[c] : dwk[c - d]) = s;
+        (blockIdx.y ? dwk : dwq)[c] = s;
     }
 }
 
@@ -307,38 +332,67 @@ cudaError_t launch_l(const RopeParams &p, int mode, int64_t grid, cudaStream_t s
 template <int DT>
 cudaError_t launch_t(const RopeParams &p, int mode, int64_t grid, cudaStream_t s)
 {
-    if (p.d <= 32) return launch_l<DT, 4>(p, mode, grid, s);
-    if (p.d <= 64) return launch_l<DT, 8>(p, mode, grid, s);
-    if (p.d <= 128) return launch_l<DT, 16>(p, mode, grid, s);
-    return launch_l<DT, 32>(p, mode, grid, s);
+    if (p.d <= 32) return launch_l<DT, 2>(p, mode, grid, s);
+    if (p.d <= 64) return launch_l<DT, 4>(p, mode, grid, s);
+    if (p.d <= 128) return launch_l<DT, 8>(p, mode, grid, s);
+    return launch_l<DT, 16>(p, mode, grid, s);
 }
+
+// Lanes a row, groups a CTA.
+int lanes_of(int d) { return d <= 32 ? 2 : (d <= 64 ? 4 : (d <= 128 ? 8 : 16)); }
+int groups_of(int d) { return THREADS / lanes_of(d); }
 
 }  // namespace
 
-int rope_tile(int64_t tokens)
+RopeSplit rope_split(int64_t tokens, int rows, int d)
 {
-    // tokens a CTA takes: 8, fewer while that leaves under eight CTAs an SM
-    int tile = MAX_TOKENS;
-    while (tile > 1 && tokens / tile < 8ll * sm_count()) tile /= 2;
-    return tile;
+    // Rows of a token that one group takes: all of them, unless that leaves fewer groups than the SMs
+    // hold at a time (3 CTAs of 256 threads); never fewer than U, since a group has its angles to compute
+    // and its weights to load first (twice the groups at n = 12288: 65 us in place of 55).
+    RopeSplit s;
+    const int64_t groups = 3ll * sm_count() * groups_of(d);
+    int64_t parts = (groups + tokens - 1) / tokens;
+    const int64_t most = (rows + U - 1) / U;
+    if (parts > most) parts = most;
+    s.run = static_cast<int>((rows + parts - 1) / parts + U - 1) / U * U;
+    s.parts = (rows + s.run - 1) / s.run;
+    s.items = tokens * s.parts;
+    s.ctas = (s.items + groups_of(d) - 1) / groups_of(d);
+    return s;
 }
 
-int64_t rope_bwd_ctas(int64_t tiles)
+RopeCtas rope_bwd_ctas(int64_t tokens, int heads, int kv, int d)
 {
-    const int64_t cap = 4ll * sm_count();
-    return tiles < cap ? tiles : cap;
+    // Two CTAs an SM that walk, or fewer where the rows run out, dealt out by the rows of each kind.
+    const int64_t q = rope_split(tokens, heads, d).ctas, k = rope_split(tokens, kv, d).ctas;
+    const int64_t cap = 2ll * sm_count(), share = (cap * kv + (heads + kv) / 2) / (heads + kv);
+    const int64_t kc = share < 1 ? 1 : (share > cap - 1 ? cap - 1 : share);
+    return {q < cap - kc ? q : cap - kc, k < kc ? k : kc};
 }
 
 cudaError_t launch_rope(RopeParams &p, int dtype, int mode, float *dwq, float *dwk, cudaStream_t s)
 {
-    p.tile = rope_tile(p.batch * p.n);
-    p.tiles = (p.n + p.tile - 1) / p.tile;
-    const int64_t all = p.batch * p.tiles, grid = mode == ROPE_BWD ? rope_bwd_ctas(all) : all;
-    cudaError_t e = dtype == ST_BF16   ? launch_t<ST_BF16>(p, mode, grid, s)
-                    : dtype == ST_FP16 ? launch_t<ST_FP16>(p, mode, grid, s)
-                                       : launch_t<ST_FP32>(p, mode, grid, s);
-    if (e != cudaSuccess || mode != ROPE_BWD || !p.wq) return e;
-    rope_dw_kernel<<<static_cast<unsigned>((2 * p.d + 31) / 32), 1024, 0, s>>>(p.partial, static_cast<int32_t>(grid), p.d, dwq, dwk);
+    const int64_t tokens = p.batch * p.n;
+    const bool bwd = mode == ROPE_BWD;
+    const RopeSplit r = rope_split(tokens, p.heads + (bwd ? 0 : p.kv + (mode == ROPE_APPEND ? p.kv : 0)), p.d);
+    p.run = r.run;
+    p.parts = r.parts;
+    p.items = r.items;
+    int64_t ctas = r.ctas;
+    if (bwd) {
+        const RopeSplit k = rope_split(tokens, p.kv, p.d);
+        p.run_k = k.run;
+        p.parts_k = k.parts;
+        p.items_k = k.items;
+        const RopeCtas c = rope_bwd_ctas(tokens, p.heads, p.kv, p.d);
+        p.q_ctas = static_cast<int32_t>(c.q);
+        ctas = c.q + c.k;
+    }
+    cudaError_t e = dtype == ST_BF16   ? launch_t<ST_BF16>(p, mode, ctas, s)
+                    : dtype == ST_FP16 ? launch_t<ST_FP16>(p, mode, ctas, s)
+                                       : launch_t<ST_FP32>(p, mode, ctas, s);
+    if (e != cudaSuccess || !bwd || !p.wq) return e;
+    rope_dw_kernel<<<dim3((p.d + 31) / 32, 2), 1024, 0, s>>>(p.partial, p.q_ctas, static_cast<int32_t>(ctas), p.d, dwq, dwk);
     return cudaGetLastError();
 }
 

@@ -17,19 +17,30 @@ struct RopeParams {
     RopeTensor gq, gk;         // backward: gradients of the outputs
     RopeTensor qo, ko, vo;     // outputs (append: ko, vo are the pages, batch = page)
     const void *wq, *wk;       // [d] weights or NULL
-    const double *turns;       // [rot / 2]
+    const uint64_t *turns;     // [rot / 2], 2^-64 turns per position
     const int32_t *positions;  // or NULL: start + t
     const int32_t *slots;      // append
-    int64_t n, start, pos_batch, tiles, page_size, nslots;
-    int64_t batch;
-    int32_t heads, kv, d, rot, interleaved, tile, w_f32;
+    int64_t n, start, pos_batch, page_size, nslots;
+    int64_t batch, items;      // items: (token, run of its rows)
+    int32_t heads, kv, d, rot, interleaved, w_f32;
+    int32_t run, parts;        // rows of a run, runs of a token
+    int64_t items_k;           // backward: of the keys (the others: of the queries)
+    int32_t run_k, parts_k, q_ctas;
     float eps, mscale, inv_d;
-    float *partial;            // backward: [CTAs, 2, d] partial weight gradients
+    float *partial;            // backward: [CTAs, d] partial weight gradients
 };
 
-// Tokens a CTA takes at a time, and the CTAs of a backward over `tiles` tiles.
-int rope_tile(int64_t tokens);
-int64_t rope_bwd_ctas(int64_t tiles);
+// How `tokens` tokens of `rows` head rows are dealt out.
+struct RopeSplit {
+    int32_t run, parts;
+    int64_t items, ctas;
+};
+RopeSplit rope_split(int64_t tokens, int rows, int d);
+// CTAs of a backward for the queries and for the keys.
+struct RopeCtas {
+    int64_t q, k;
+};
+RopeCtas rope_bwd_ctas(int64_t tokens, int heads, int kv, int d);
 cudaError_t launch_rope(RopeParams &p, int dtype, int mode, float *dwq, float *dwk, cudaStream_t s);
 
 }  // namespace st

@@ -378,8 +378,8 @@ ST_API st_status_t st_window_bwd(const void *q, const void *k, const void *v, co
 /* ---- norms of queries and keys per head, with the position rotation -------------------------- */
 typedef enum { ST_ROPE_NONE = 0, ST_ROPE_LINEAR = 1, ST_ROPE_NTK = 2, ST_ROPE_YARN = 3 } st_rope_scaling_t;
 
-/* Rotation speeds (host only): turns[i] = w_i / 2 pi, i < rot / 2, in turns per position, with
- * w_i = base^(-2i / rot), and the factor *mscale on cos and sin (1 except for YARN).  Scaling by
+/* Rotation speeds (host only): turns[i] = 2^64 w_i / 2 pi, i < rot / 2, in units of 2^-64 turns per
+ * position, with w_i = base^(-2i / rot), and the factor *mscale on cos and sin (1 except for YARN).  Scaling by
  * `factor` s >= 1 for contexts s times the `original` one:
  *   LINEAR  w_i / s (positions interpolated)
  *   NTK     base s^(rot / (rot - 2)): the slowest pair slows by s, the fastest keeps its speed
@@ -387,11 +387,11 @@ typedef enum { ST_ROPE_NONE = 0, ST_ROPE_LINEAR = 1, ST_ROPE_NTK = 2, ST_ROPE_YA
  *           t = clamp((r_i - 1) / (32 - 1), 0, 1), w_i (t + (1 - t) / s); mscale = 0.1 ln s + 1
  * Errors: ST_ERR_INVALID_ARG (NULL, rot odd or < 2 (NTK: < 4), base <= 1, factor < 1, original <= 0). */
 ST_API st_status_t st_rope_turns(int32_t rot, double base, int32_t scaling, double factor, double original,
-                                 double *turns, float *mscale);
+                                 uint64_t *turns, float *mscale);
 
 /* Shapes of a norm-and-rotation call.  q and q_out: [batch, heads, n, d]; k and k_out: [batch,
  * kv_heads, n, d]; in the backward the *_out strides are those of the output gradients, and dq, dk
- * those of the input gradients.  d: a multiple of 8 up to 256; rot: a multiple of 16, 16 .. d;
+ * those of the input gradients.  d: a multiple of 16 up to 256; rot: a multiple of 16, 16 .. d;
  * dtype: ST_BF16, ST_FP16 or ST_FP32; wdtype: type of wq and wk (dtype or ST_FP32).
  * positions: int32, element (b, t) at b * pos_batch + t (pos_batch 0: shared by the batch). */
 typedef struct {
@@ -402,22 +402,23 @@ typedef struct {
 } st_rope_desc_t;
 
 /* Per head row x of q or k: y = x / sqrt(mean(x^2) + eps) * w (wq, wk: [d] weights, or both NULL:
- * no norm), then the rotation of the first `rot` elements by the angle a_i = 2 pi pos turns[i]:
+ * no norm), then the rotation of the first `rot` elements by the angle a_i = pos w_i:
  *   half layout (interleaved 0): pairs (i, i + rot/2);  interleaved: pairs (2i, 2i + 1)
  *   (y0, y1) -> mscale (y0 cos a - y1 sin a, y1 cos a + y0 sin a)
- * pos = positions[b, t], or start + t when positions is NULL.  Angles are reduced in 64 bits, so far
- * positions keep their accuracy.  fp32 arithmetic, rounded once.  turns: device fp64 [rot / 2].
+ * pos = positions[b, t], or start + t when positions is NULL.  Angles are products of 64-bit
+ * integers modulo a turn, so far positions keep their accuracy.  fp32 arithmetic, rounded once.  turns:
+ * device [rot / 2].
  * q_out may be q and k_out may be k (same strides).  Errors: ST_ERR_INVALID_ARG, ST_ERR_UNSUPPORTED,
  * ST_ERR_ALIGNMENT, ST_ERR_CUDA. */
 ST_API st_status_t st_qk_norm_rope(const void *q, const void *k, const void *wq, const void *wk,
-                                   const double *turns, const int32_t *positions, void *q_out, void *k_out,
+                                   const uint64_t *turns, const int32_t *positions, void *q_out, void *k_out,
                                    const st_rope_desc_t *desc, st_stream_t stream);
 
 /* Gradients: gq, gk of the outputs; dq, dk of the inputs (dq may be gq, dk may be gk, same strides);
  * dwq, dwk: [d] fp32 (NULL without weights), summed in a fixed order. */
 ST_API size_t st_qk_norm_rope_bwd_workspace_bytes(const st_rope_desc_t *desc);
 ST_API st_status_t st_qk_norm_rope_bwd(const void *q, const void *k, const void *gq, const void *gk,
-                                       const void *wq, const void *wk, const double *turns,
+                                       const void *wq, const void *wk, const uint64_t *turns,
                                        const int32_t *positions, void *dq, void *dk, float *dwq, float *dwk,
                                        void *workspace, size_t workspace_bytes, const st_rope_desc_t *desc,
                                        st_stream_t stream);
@@ -467,7 +468,7 @@ ST_API st_status_t st_paged_plan(const int32_t *lens, const int32_t *new_tokens,
  * the cache are left as they were.  Slots must be distinct: of two tokens with one slot either may
  * be stored, in part. */
 ST_API st_status_t st_paged_append(const void *q, const void *k, const void *v, const void *wq, const void *wk,
-                                   const double *turns, const int32_t *positions, const int32_t *slots,
+                                   const uint64_t *turns, const int32_t *positions, const int32_t *slots,
                                    void *q_out, void *k_pages, void *v_pages, const st_strides_t *v_strides,
                                    const st_pages_t *pages, const st_rope_desc_t *desc, st_stream_t stream);
 
