@@ -311,7 +311,11 @@ st_status_t check_paged(const st_paged_desc_t *d, const st_window_t *w)
     return ST_OK;
 }
 
-int32_t paged_grid() { return st::sm_count() * st::PD_CTAS_PER_SM; }
+int32_t paged_grid()
+{
+    const int32_t n = st::sm_count() * st::PD_CTAS_PER_SM;
+    return n < st::PD_MAX_GRID ? n : st::PD_MAX_GRID;
+}
 
 }  // namespace
 

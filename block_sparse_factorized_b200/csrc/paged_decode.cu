@@ -18,9 +18,10 @@
 //   - One launch splits everything evenly: with tiles of 16 keys numbered request by request, key
 //     head by key head, each CTA takes an equal run of them, whatever the lengths are; rows that
 //     cross CTAs leave (m, L, O) parts, which a second, overlapped launch joins in order.
-//   - P is split into two 16-bit parts for bf16 (hi + lo, 16 bits of mantissa together): rounding it
-//     to 8 bits would cost as much accuracy as the output's own rounding, and the second product
-//     hides behind the loads.  fp16's 11 bits are kept as they are.
+//   - With bf16 and at most 8 heads P goes in as two 16-bit parts (hi + lo, 16 bits of mantissa
+//     together), the second in the rows 8 .. 15 that would be empty; rounding it to 8 bits would cost
+//     as much accuracy as the output's own rounding.  With more heads it is rounded to 8 bits (a second
+//     product would cost 13% of the kernel's time), and fp16's 11 bits are kept as they are.
 #include "elem.cuh"
 #include "kernels.h"
 #include "lm.h"
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(THREADS, PD_CTAS_PER_SM) paged_kernel(const __
                 if (g + 8 * i < nh)
                     qf[i][k] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + (qrow + g + 8 * i) * D + 32 * k + 8 * c);
             }
-        float o[VB * 8][2 * RW], m[RW], l[RW];
+        float o[VB * 8][RW == 1 ? 2 : 4], m[RW], l[RW];
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
             m[i] = -INFINITY;
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(THREADS, PD_CTAS_PER_SM) paged_kernel(const __
 #pragma unroll
         for (int j = 0; j < VB * 8; ++j)
 #pragma unroll
-            for (int e = 0; e < 2 * RW; ++e) o[j][e] = 0.f;
+            for (int e = 0; e < (RW == 1 ? 2 : 4); ++e) o[j][e] = 0.f;
 
         const char *kh = p.k + hk * p.k_head, *vh = p.v + hk * p.v_head;
         const int32_t *table = p.table + r * p.table_stride;
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(THREADS, PD_CTAS_PER_SM) paged_kernel(const __
                     const float p0 = ex2(s[n][2 * i] - base), p1 = ex2(s[n][2 * i + 1] - base);
                     l[i] += p0 + p1;
                     hi[i][n] = pack16<DT>(p0, p1);
-                    if constexpr (DT == ST_BF16) lo[i][n] = pack16<DT>(p0 - bf16_lo(hi[i][n]), p1 - bf16_hi(hi[i][n]));
+                    if constexpr (DT == ST_BF16 && RW == 1) lo[i][n] = pack16<DT>(p0 - bf16_lo(hi[i][n]), p1 - bf16_hi(hi[i][n]));
                 }
             }
             // O += P V: value column 8n + j of each 64 in step j
@@ -260,15 +261,19 @@ __global__ void __launch_bounds__(THREADS, PD_CTAS_PER_SM) paged_kernel(const __
                     auto word = [&](const uint4 &x) { return j < 2 ? x.x : (j < 4 ? x.y : (j < 6 ? x.z : x.w)); };
                     const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
                     const uint32_t b0 = __byte_perm(word(vf[b][0]), word(vf[b][1]), sel), b1 = __byte_perm(word(vf[b][2]), word(vf[b][3]), sel);
-                    float acc[4] = {o[b * 8 + j][0], o[b * 8 + j][1], RW > 1 ? o[b * 8 + j][2 * RW - 2] : 0.f, RW > 1 ? o[b * 8 + j][2 * RW - 1] : 0.f};
-                    mma<DT>(acc, hi[0][0], RW > 1 ? hi[RW - 1][0] : 0u, hi[0][1], RW > 1 ? hi[RW - 1][1] : 0u, b0, b1);
-                    if constexpr (DT == ST_BF16)
-                        mma<DT>(acc, lo[0][0], RW > 1 ? lo[RW - 1][0] : 0u, lo[0][1], RW > 1 ? lo[RW - 1][1] : 0u, b0, b1);
-                    o[b * 8 + j][0] = acc[0];
-                    o[b * 8 + j][1] = acc[1];
-                    if constexpr (RW > 1) {
-                        o[b * 8 + j][2] = acc[2];
-                        o[b * 8 + j][3] = acc[3];
+                    if constexpr (RW == 1) {
+                        float acc[4] = {o[b * 8 + j][0], o[b * 8 + j][1], 0.f, 0.f};
+                        if constexpr (DT == ST_BF16) {  // rows 8 .. 15: the low parts of the same heads
+                            mma<DT>(acc, hi[0][0], lo[0][0], hi[0][1], lo[0][1], b0, b1);
+                            o[b * 8 + j][0] = acc[0] + acc[2];
+                            o[b * 8 + j][1] = acc[1] + acc[3];
+                        } else {
+                            mma<DT>(acc, hi[0][0], 0u, hi[0][1], 0u, b0, b1);
+                            o[b * 8 + j][0] = acc[0];
+                            o[b * 8 + j][1] = acc[1];
+                        }
+                    } else {
+                        mma<DT>(o[b * 8 + j], hi[0][0], hi[RW - 1][0], hi[0][1], hi[RW - 1][1], b0, b1);
                     }
                 }
         }
@@ -325,11 +330,16 @@ __global__ void __launch_bounds__(THREADS, PD_CTAS_PER_SM) paged_kernel(const __
 }
 
 // Join the parts of the row that CTA blockIdx.x + 1's first tile lies inside, if no earlier CTA's
-// first tile does.  blockIdx.y: head of the block; one thread per two elements.
+// first tile does.  blockIdx.y: head of the block.  The parts' weights first, one a thread, then their
+// O in groups of D / 2 threads (two elements each), the groups' sums added in order.
+constexpr int JOIN_THREADS = 256;
+
 template <int DT, int D, int HB>
-__global__ void __launch_bounds__(D / 2) paged_join_kernel(const __grid_constant__ PagedParams p)
+__global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_constant__ PagedParams p)
 {
-    constexpr int PART = HB * (D + 2);
+    constexpr int PART = HB * (D + 2), NG = JOIN_THREADS / (D / 2);
+    __shared__ float weight[PD_MAX_GRID];
+    __shared__ float red[JOIN_THREADS / 32], sum_o[NG][D + 2];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int R = p.requests, rows_per = p.kv * p.blocks;
     const int64_t all = static_cast<int64_t>(p.prefix[R]) * rows_per, per = share_of(all, p.grid);
@@ -343,22 +353,52 @@ __global__ void __launch_bounds__(D / 2) paged_join_kernel(const __grid_constant
     if (cut == row0 || cut - per > row0) return;  // a row's first tile, or an earlier CTA's row
     const int hk = row / p.blocks, hb = row - hk * p.blocks, h = blockIdx.y;
     if (h >= min(HB, p.group - hb * HB)) return;
-    // CTAs c0 .. c1 hold the row's parts; a CTA's run is its first (slot 0) where the row covers the
+    // CTAs c0 .. c0 + n - 1 hold the row's parts; a CTA's is its first (slot 0) where the row covers the
     // CTA's first tile
-    const int64_t c0 = row0 / per, c1 = (end - 1) / per;
-    const int x = 2 * threadIdx.x;
+    const int64_t c0 = row0 / per;
+    const int n = static_cast<int>((end - 1) / per - c0) + 1;
+    auto part_of = [&](int i) { return p.parts + (2 * (c0 + i) + ((c0 + i) * per >= row0 ? 0 : 1)) * PART; };
+    auto block_reduce = [&](float x, bool max) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float y = __shfl_xor_sync(0xffffffffu, x, o);
+            x = max ? fmaxf(x, y) : x + y;
+        }
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+        __syncthreads();
+        x = red[0];
+        for (int w = 1; w < JOIN_THREADS / 32; ++w) x = max ? fmaxf(x, red[w]) : x + red[w];
+        return x;
+    };
     float m = -INFINITY;
-    for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, p.parts[(2 * c + (c * per >= row0 ? 0 : 1)) * PART + h]);
+    for (int i = threadIdx.x; i < n; i += JOIN_THREADS) {
+        weight[i] = part_of(i)[h];
+        m = fmaxf(m, weight[i]);
+    }
+    m = block_reduce(m, true);
     const float base = m == -INFINITY ? 0.f : m;
-    float sum = 0.f, o0 = 0.f, o1 = 0.f;
+    float sum = 0.f;
+    for (int i = threadIdx.x; i < n; i += JOIN_THREADS) {
+        weight[i] = ex2(weight[i] - base);
+        sum = fmaf(weight[i], part_of(i)[HB + h], sum);
+    }
+    sum = block_reduce(sum, false);  // (also: every weight is written)
+    const int grp = threadIdx.x / (D / 2), x = 2 * (threadIdx.x % (D / 2));
+    float o0 = 0.f, o1 = 0.f;
 #pragma unroll 4
-    for (int64_t c = c0; c <= c1; ++c) {
-        const float *part = p.parts + (2 * c + (c * per >= row0 ? 0 : 1)) * PART;
-        const float f = ex2(part[h] - base);
-        const float2 o = *reinterpret_cast<const float2 *>(part + 2 * HB + h * D + x);
-        sum = fmaf(f, part[HB + h], sum);
-        o0 = fmaf(f, o.x, o0);
-        o1 = fmaf(f, o.y, o1);
+    for (int i = grp; i < n; i += NG) {
+        const float2 o = *reinterpret_cast<const float2 *>(part_of(i) + 2 * HB + h * D + x);
+        o0 = fmaf(weight[i], o.x, o0);
+        o1 = fmaf(weight[i], o.y, o1);
+    }
+    sum_o[grp][x] = o0;
+    sum_o[grp][x + 1] = o1;
+    __syncthreads();
+    if (grp != 0) return;
+    for (int i = 1; i < NG; ++i) {
+        o0 += sum_o[i][x];
+        o1 += sum_o[i][x + 1];
     }
     const int64_t q = static_cast<int64_t>(r) * p.heads + hk * p.group + hb * HB + h;
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -378,7 +418,7 @@ cudaError_t launch_h(const PagedParams &p, cudaStream_t s)
     if (p.grid == 1) return cudaSuccess;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(p.grid - 1), static_cast<unsigned>(p.group < HB ? p.group : HB));
-    cfg.blockDim = dim3(D / 2);
+    cfg.blockDim = dim3(JOIN_THREADS);
     cfg.stream = s;
     cudaLaunchAttribute a{};
     a.id = cudaLaunchAttributeProgrammaticStreamSerialization;

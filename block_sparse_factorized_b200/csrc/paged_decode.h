@@ -7,6 +7,7 @@ namespace st {
 
 constexpr int PD_TILE = 16;             // keys a warp takes at a time
 constexpr int PD_CTAS_PER_SM = 3;
+constexpr int PD_MAX_GRID = 1024;       // CTAs at most: a row's parts have their weights in shared memory
 constexpr int PD_MAX_REQUESTS = 8192;   // the tile prefix sums live in shared memory
 
 struct PagedParams {
