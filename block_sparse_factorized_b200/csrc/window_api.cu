@@ -172,7 +172,7 @@ st_status_t st_window_bwd(const void *q, const void *k, const void *v, const voi
     const Units u = plan_units(p.g);
     const BwdSizes z = bwd_sizes(p.g, u, desc->d);
     if (static_cast<int64_t>(u.entries) * p.g.batch * p.g.kv > INT32_MAX ||
-        static_cast<int64_t>(u.split) * p.g.batch * p.g.kv * 2 > INT32_MAX)
+        static_cast<int64_t>(u.split) * p.g.batch * p.g.kv * (desc->d / 4) > INT32_MAX)
         return ST_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < z.total()) return ST_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return ST_ERR_ALIGNMENT;

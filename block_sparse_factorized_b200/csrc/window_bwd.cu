@@ -52,6 +52,8 @@ __device__ __forceinline__ int32_t tile_steps(const WindowGeom &g, int32_t t, in
 // ---- preparation ------------------------------------------------------------------------------
 // D_i (0 for padding rows), the unit list of dk_dv (block 0: the chunked key tiles first), and for fp16 the largest squared norms
 // of live dO and V rows.  D / 8 lanes a row; memory-bound.
+constexpr int PRE_ROWS = 256;
+
 template <int DT, int D>
 __global__ void __launch_bounds__(256) window_pre_kernel(const __grid_constant__ WindowBwdParams p)
 {
@@ -87,52 +89,55 @@ __global__ void __launch_bounds__(256) window_pre_kernel(const __grid_constant__
         }
         return;
     }
-    const int l = threadIdx.x % L;
-    const int64_t rows = static_cast<int64_t>(g.batch) * g.heads * g.nq, vrows = DT == ST_FP16 ? static_cast<int64_t>(g.batch) * g.kv * g.nk : 0;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x - 1) * NG; base < rows + vrows; base += static_cast<int64_t>(gridDim.x - 1) * NG) {
-        const int64_t r = base + threadIdx.x / L;
-        float dot = 0.f, sq = 0.f;
-        bool live = false;
-        int64_t b = 0, h = 0;
-        if (r < rows) {
-            const int64_t bh = r / g.nq, i = r - bh * g.nq;
-            b = bh / g.heads;
-            h = bh - b * g.heads;
-            live = g.q_start + i < window_len(g, static_cast<int32_t>(b));
-            if (live) {
-                float x[8], y[8];
-                widen8<DT>(load8<DT>(p.oraw.p + b * p.oraw.batch + h * p.oraw.head + i * p.oraw.row + 16 * l), x);
-                widen8<DT>(load8<DT>(p.doraw.p + b * p.doraw.batch + h * p.doraw.head + i * p.doraw.row + 16 * l), y);
+    // 256 rows of one (batch, head) of dO and O, or of one (batch, key head) of V, a CTA
+    const int l = threadIdx.x % L, grp = threadIdx.x / L;
+    const int32_t qc = (g.nq + PRE_ROWS - 1) / PRE_ROWS, vc = (g.nk + PRE_ROWS - 1) / PRE_ROWS;
+    int64_t i = blockIdx.x - 1;
+    const bool is_v = i >= static_cast<int64_t>(g.batch) * g.heads * qc;
+    if (is_v) i -= static_cast<int64_t>(g.batch) * g.heads * qc;
+    const int32_t per = is_v ? vc : qc, heads = is_v ? g.kv : g.heads, n = is_v ? g.nk : g.nq;
+    const int32_t bh = static_cast<int32_t>(i / per), row0 = static_cast<int32_t>(i - static_cast<int64_t>(bh) * per) * PRE_ROWS;
+    const int32_t b = bh / heads, h = bh - b * heads;
+    const int32_t live = min(n, window_len(g, b) - (is_v ? 0 : g.q_start));  // rows before the sequence's end
+    const RawTensor &y = is_v ? p.vraw : p.doraw;
+    const char *yp = y.p + b * y.batch + h * y.head + 16 * l, *op = p.oraw.p + b * p.oraw.batch + h * p.oraw.head + 16 * l;
+    float *delta = p.delta + static_cast<int64_t>(bh) * g.nq;
+    float most = 0.f;
+    for (int r0 = 0; r0 < PRE_ROWS; r0 += 4 * NG) {
+        Vec8<DT> vy[4], vo[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    dot = fmaf(x[e], y[e], dot);
-                    sq = fmaf(y[e], y[e], sq);
-                }
-            }
-        } else if (r < rows + vrows) {
-            const int64_t bh = (r - rows) / g.nk, j = (r - rows) - bh * g.nk;
-            b = bh / g.kv;
-            h = bh - b * g.kv;
-            live = j < window_len(g, static_cast<int32_t>(b));
-            if (live) {
-                float y[8];
-                widen8<DT>(load8<DT>(p.vraw.p + b * p.vraw.batch + h * p.vraw.head + j * p.vraw.row + 16 * l), y);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sq = fmaf(y[e], y[e], sq);
+        for (int u = 0; u < 4; ++u) {
+            const int32_t r = row0 + r0 + u * NG + grp;
+            vy[u].r[0] = vo[u].r[0] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < live) {
+                vy[u] = load8<DT>(yp + r * y.row);
+                if (!is_v) vo[u] = load8<DT>(op + r * p.oraw.row);
             }
         }
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) {
-            dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            if (DT == ST_FP16) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        for (int u = 0; u < 4; ++u) {
+            const int32_t r = row0 + r0 + u * NG + grp;
+            float a[8], c[8], dot = 0.f, sq = 0.f;
+            widen8<DT>(vy[u], a);
+            widen8<DT>(vo[u], c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dot = fmaf(a[e], c[e], dot);
+                sq = fmaf(a[e], a[e], sq);
+            }
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) {
+                dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                if (DT == ST_FP16) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+            }
+            if (!is_v && l == 0 && r < g.nq) delta[r] = dot;  // (0 for padding rows: nothing was loaded)
+            if (DT == ST_FP16) most = sq > most || sq != sq ? sq : most;  // a NaN stays
         }
-        if (l != 0) continue;
-        if (r < rows) p.delta[r] = live ? dot : 0.f;
-        if (DT == ST_FP16 && live) {  // non-negative floats (NaN above all) order as integers
-            uint32_t *m = p.maxima + 2 * (b * g.kv + (r < rows ? h / g.group : h)) + (r < rows ? 0 : 1);
-            const uint32_t u = __float_as_uint(sq) & 0x7FFFFFFFu;
-            if (u > *reinterpret_cast<volatile uint32_t *>(m)) atomicMax(m, u);
-        }
+    }
+    if constexpr (DT == ST_FP16) {  // non-negative floats, NaN above all, order as integers
+        uint32_t u = __float_as_uint(most) & 0x7FFFFFFFu;
+        u = __reduce_max_sync(0xffffffffu, u);
+        if ((threadIdx.x & 31) == 0) atomicMax(p.maxima + 2 * (b * g.kv + (is_v ? h : h / g.group)) + (is_v ? 1 : 0), u);
     }
 }
 
@@ -529,35 +534,34 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
     }
 }
 
-// dK, dV of the key tiles cut into chunks: their partials added in chunk order.
+// dK, dV of the key tiles cut into chunks: their partials added in chunk order.  A thread takes 8
+// columns of one key row.
 template <int DT, int D>
-__global__ void __launch_bounds__(256) window_join_kernel(const __grid_constant__ WindowBwdParams p)
+__global__ void __launch_bounds__(128) window_join_kernel(const __grid_constant__ WindowBwdParams p)
 {
     const WindowGeom &g = p.g;
-    const int32_t e = blockIdx.x % p.nsplit, bo = blockIdx.x / p.nsplit, bh = bo >> 1, out = bo & 1;
+    const uint32_t e = blockIdx.x % static_cast<uint32_t>(p.nsplit), bo = blockIdx.x / static_cast<uint32_t>(p.nsplit);
+    const int32_t ch = static_cast<int32_t>(bo % (D / 8)), out = static_cast<int32_t>(bo / (D / 8) & 1), bh = static_cast<int32_t>(bo / (D / 4));
     const int2 en = p.entries[e];
-    if (en.y != 0) return;  // one block a key tile: at its first chunk
+    if (en.y != 0) return;  // once a key tile: at its first chunk
     int32_t i0;
-    const int32_t n = chunks_of(tile_steps(g, en.x, i0), p.chunk);
+    const int32_t n = chunks_of(tile_steps(g, en.x, i0), p.chunk), row = threadIdx.x, kpos = en.x * 128 + row;
+    if (kpos >= g.nk) return;
     const int64_t slot = static_cast<int64_t>(bh) * p.nsplit + e;
     const int32_t b = bh / g.kv, hk = bh - b * g.kv;
     const OutTensor &t = out == 0 ? p.dv : p.dk;
-    for (int i = threadIdx.x; i < 128 * (D / 8); i += 256) {
-        const int row = i % 128, ch = i / 128, kpos = en.x * 128 + row;
-        if (kpos >= g.nk) continue;
-        float x[8];
+    float x[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = 0.f;
+    for (int q = 0; q < 8; ++q) x[q] = 0.f;
 #pragma unroll 4
-        for (int32_t c = 0; c < n; ++c) {
-            const float4 *src = reinterpret_cast<const float4 *>(p.parts) + (((slot + c) * 2 + out) * (D / 4) + 2 * ch) * 128 + row;
-            const float4 a = src[0], d = src[128];
-            x[0] += a.x; x[1] += a.y; x[2] += a.z; x[3] += a.w;
-            x[4] += d.x; x[5] += d.y; x[6] += d.z; x[7] += d.w;
-        }
-        *reinterpret_cast<uint4 *>(t.p + b * t.batch + hk * t.head + kpos * t.row + 16 * ch) =
-            make_uint4(pack16<DT>(x[0], x[1]), pack16<DT>(x[2], x[3]), pack16<DT>(x[4], x[5]), pack16<DT>(x[6], x[7]));
+    for (int32_t c = 0; c < n; ++c) {
+        const float4 *src = reinterpret_cast<const float4 *>(p.parts) + (((slot + c) * 2 + out) * (D / 4) + 2 * ch) * 128 + row;
+        const float4 a = src[0], d = src[128];
+        x[0] += a.x; x[1] += a.y; x[2] += a.z; x[3] += a.w;
+        x[4] += d.x; x[5] += d.y; x[6] += d.z; x[7] += d.w;
     }
+    *reinterpret_cast<uint4 *>(t.p + b * t.batch + hk * t.head + kpos * t.row + 16 * ch) =
+        make_uint4(pack16<DT>(x[0], x[1]), pack16<DT>(x[2], x[3]), pack16<DT>(x[4], x[5]), pack16<DT>(x[6], x[7]));
 }
 
 // ---- dQ ---------------------------------------------------------------------------------------
@@ -893,15 +897,15 @@ cudaError_t launch(const WindowBwdParams &p, cudaStream_t s)
     const WindowGeom &g = p.g;
     const int64_t cap = sm_count();
     if (DT == ST_FP16 && (e = cudaMemsetAsync(p.maxima, 0, sizeof(uint32_t) * 2 * g.batch * g.kv, s)) != cudaSuccess) return e;
-    const int64_t rows = static_cast<int64_t>(g.batch) * g.heads * g.nq, groups = (rows + 256 / (D / 8) - 1) / (256 / (D / 8));
-    const int64_t pre = groups < 16 * cap ? groups : 16 * cap;
-    window_pre_kernel<DT, D><<<static_cast<unsigned>(pre + 1), 256, 0, s>>>(p);
+    int64_t pre = 1 + static_cast<int64_t>(g.batch) * g.heads * ((g.nq + PRE_ROWS - 1) / PRE_ROWS);
+    if (DT == ST_FP16) pre += static_cast<int64_t>(g.batch) * g.kv * ((g.nk + PRE_ROWS - 1) / PRE_ROWS);
+    window_pre_kernel<DT, D><<<static_cast<unsigned>(pre), 256, 0, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t ku = static_cast<int64_t>(p.nentries) * g.batch * g.kv, qu = static_cast<int64_t>(g.batch) * g.heads * g.nqt;
     window_dkdv_kernel<DT, D><<<static_cast<unsigned>(ku < cap ? ku : cap), THREADS, KCfg<D>::SMEM, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.nsplit > 0) {
-        window_join_kernel<DT, D><<<static_cast<unsigned>(p.nsplit) * g.batch * g.kv * 2, 256, 0, s>>>(p);
+        window_join_kernel<DT, D><<<static_cast<unsigned>(p.nsplit) * g.batch * g.kv * (D / 4), 128, 0, s>>>(p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     window_dq_kernel<DT, D><<<static_cast<unsigned>(qu < cap ? qu : cap), THREADS, QCfg<D>::SMEM, s>>>(p);
