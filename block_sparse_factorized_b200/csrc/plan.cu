@@ -7,38 +7,41 @@
 // is free_pages[free - 1 - (c_r + i)]: a page depends on prefix sums only, never on another request's
 // result, so one launch does it all.
 //
-// Bound by latency (tens of kilobytes): every CTA computes both prefix sums over all requests for
-// itself, in shared memory, which costs less than a second launch or a grid barrier; the tokens and
-// the new pages are then dealt out over the CTAs, each finding its request by bisection.
+// Bound by latency (tens of kilobytes): every CTA computes the prefix sums over all requests for itself,
+// in shared memory, a run of requests a thread and one scan over the threads for each sum, which costs
+// less than a second launch or a grid barrier; the tokens and the new pages are then dealt out over the
+// CTAs, each finding its request by bisection.
+#include "kernels.h"
 #include "lm.h"
 #include "plan.h"
 
 namespace st {
 namespace {
 
-constexpr int THREADS = 1024;
-
-// Inclusive prefix sum over the CTA, on top of `carry` (which becomes the total so far).
-__device__ __forceinline__ int64_t scan(int64_t x, int64_t &carry, int64_t *warp_sums)
+// Exclusive prefix sum over the CTA; `all` gets the total.
+template <int THREADS>
+__device__ __forceinline__ int64_t scan(int64_t x, int64_t &all, int64_t *sums)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t incl = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
     }
     __syncthreads();  // the previous scan's sums are no longer read
-    if (lane == 31) warp_sums[warp] = x;
+    if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    int64_t before = carry, all = carry;
-#pragma unroll 8
-    for (int w = 0; w < THREADS / 32; ++w) {
-        const int64_t s = warp_sums[w];
-        if (w < warp) before += s;
-        all += s;
+    // every warp scans the warps' sums
+    int64_t w = lane < THREADS / 32 ? sums[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < THREADS / 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
     }
-    carry = all;
-    return before + x;
+    all = __shfl_sync(0xffffffffu, w, THREADS / 32 - 1);
+    const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    return (warp > 0 ? before : 0) + incl - x;
 }
 
 // The request r whose run [first[r], first[r + 1]) holds x; first[] rises from 0 past x.
@@ -55,47 +58,75 @@ __device__ __forceinline__ int find(const int32_t *first, int n, int64_t x)
 
 __device__ __forceinline__ int32_t clamp32(int64_t x) { return x > INT32_MAX ? INT32_MAX : static_cast<int32_t>(x); }
 
+template <int THREADS>
 __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ PlanParams p)
 {
     extern __shared__ int32_t sm[];
-    __shared__ int64_t warp_sums[THREADS / 32];
+    __shared__ int64_t sums[THREADS / 32];
     const int R = p.requests;
     int32_t *offset = sm;              // [R + 1] first token
     int32_t *taken = sm + R + 1;       // [R + 1] pages taken by earlier requests (served ones)
     int32_t *asked = sm + 2 * (R + 1); // [R] pages asked for by earlier requests; -1: not served
-    const int64_t s = p.page_size;
-    int64_t free = *p.free_count;
-    free = free < 0 ? 0 : (free > p.free_capacity ? p.free_capacity : free);
-    int64_t tok = 0, ask = 0, got = 0;
-    for (int base = 0; base < R; base += THREADS) {
-        const int r = base + threadIdx.x;
-        const bool in = r < R;
-        const int64_t a = in ? p.lens[r] : 0, bn = in ? p.new_tokens[r] : 0, b = bn > 0 ? bn : 0;
-        const int64_t t1 = scan(b, tok, warp_sums);
-        const int64_t held = a > 0 ? (a + s - 1) / s : 0, want = a >= 0 ? (a + b + s - 1) / s : 0;
-        const bool fits = in && a >= 0 && bn >= 0 && want <= p.max_pages && t1 <= p.tokens &&
-                          a + b <= INT32_MAX;
-        const int64_t need = fits ? want - held : 0;
-        const int64_t c1 = scan(need, ask, warp_sums);
-        const bool served = fits && (need == 0 || c1 <= free);
-        const int64_t g1 = scan(served ? need : 0, got, warp_sums);
-        if (in) {
-            offset[r] = clamp32(t1 - b);
-            taken[r] = clamp32(g1 - (served ? need : 0));
-            asked[r] = served ? clamp32(c1 - need) : -1;
-            if (r == R - 1) {
-                offset[R] = clamp32(t1);
-                taken[R] = clamp32(g1);
-            }
-            if (blockIdx.x == 0) {
-                p.lens_out[r] = static_cast<int32_t>(served ? a + b : a);
-                p.status[r] = served ? 0 : 1;
-                p.offsets[r] = clamp32(t1 - b);
-                if (r == R - 1) {
-                    p.offsets[R] = clamp32(t1);
-                    *p.free_left = static_cast<int32_t>(free - g1);
-                }
-            }
+    int32_t *cached = sm + 3 * (R + 1);// [R] lens
+    const uint32_t s = static_cast<uint32_t>(p.page_size);  // positions and s together stay below 2^32
+    const int32_t count = *p.free_count;
+    const int per = (R + THREADS - 1) / THREADS, r0 = min(R, static_cast<int>(threadIdx.x) * per), r1 = min(R, r0 + per);
+    int64_t x = 0, tok, ask, got;
+    for (int r = r0; r < r1; ++r) {
+        const int32_t a = p.lens[r], b = p.new_tokens[r];
+        cached[r] = a;
+        asked[r] = b;  // for now
+        x += max(b, 0);
+    }
+    x = scan<THREADS>(x, tok, sums);
+    // pages the request holds and wants; whether it fits
+    auto look = [&](int r, int64_t first, int64_t &need) {
+        const int64_t a = cached[r], bn = asked[r], end = a + bn;
+        bool fits = a >= 0 && bn >= 0 && end <= INT32_MAX && first + bn <= p.tokens;
+        const uint32_t held = fits ? (static_cast<uint32_t>(a) + s - 1) / s : 0, want = fits ? (static_cast<uint32_t>(end) + s - 1) / s : 0;
+        fits = fits && want <= p.max_pages;
+        need = fits ? want - held : 0;
+        return fits;
+    };
+    int64_t y = 0, need;
+    for (int r = r0; r < r1; ++r) {
+        offset[r] = clamp32(x);
+        look(r, x, need);
+        x += max(asked[r], 0);
+        y += need;
+    }
+    y = scan<THREADS>(y, ask, sums);
+    const int64_t free = min(max(static_cast<int64_t>(count), int64_t(0)), p.free_capacity);
+    int64_t z = 0;
+    {
+        int64_t c = y;
+        for (int r = r0; r < r1; ++r) {
+            const bool fits = look(r, offset[r], need);
+            c += need;
+            if (fits && c <= free) z += need;
+        }
+    }
+    z = scan<THREADS>(z, got, sums);
+    for (int r = r0; r < r1; ++r) {
+        const int64_t a = cached[r];
+        const int32_t b = max(asked[r], 0);
+        const bool fits = look(r, offset[r], need), served = fits && (need == 0 || y + need <= free);
+        taken[r] = clamp32(z);
+        asked[r] = served ? clamp32(y) : -1;
+        y += need;
+        z += served ? need : 0;
+        if (blockIdx.x == 0) {
+            p.lens_out[r] = static_cast<int32_t>(served ? a + b : a);
+            p.status[r] = served ? 0 : 1;
+            p.offsets[r] = offset[r];
+        }
+    }
+    if (threadIdx.x == 0) {
+        offset[R] = clamp32(tok);
+        taken[R] = clamp32(got);
+        if (blockIdx.x == 0) {
+            p.offsets[R] = clamp32(tok);
+            *p.free_left = static_cast<int32_t>(free - got);
         }
     }
     __syncthreads();
@@ -103,7 +134,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
     // new pages into the block tables (columns past those held: no CTA reads them)
     for (int64_t k = id; k < taken[R]; k += all) {
         const int r = find(taken, R, k);
-        const int64_t i = k - taken[r], held = (static_cast<int64_t>(p.lens[r]) + s - 1) / s;
+        const int64_t i = k - taken[r], held = (static_cast<uint32_t>(cached[r]) + s - 1) / s;
         p.block_table[r * p.table_stride + held + i] = p.free_pages[free - 1 - (asked[r] + i)];
     }
     for (int64_t t = id; t < p.tokens; t += all) {
@@ -111,9 +142,9 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
         if (t < offset[R]) {
             const int r = find(offset, R, t);
             if (asked[r] >= 0) {
-                const int64_t a = p.lens[r], pos = a + (t - offset[r]), held = (a + s - 1) / s, col = pos / s;
+                const uint32_t a = cached[r], pos = a + static_cast<uint32_t>(t - offset[r]), held = (a + s - 1) / s, col = pos / s;
                 const int64_t page = col < held ? p.block_table[r * p.table_stride + col]
-                                                : p.free_pages[free - 1 - (asked[r] + col - held)];
+                                                : p.free_pages[free - 1 - (asked[r] + static_cast<int64_t>(col - held))];
                 const int64_t at = page * s + (pos - col * s);
                 pos32 = static_cast<int32_t>(pos);
                 if (page >= 0 && at <= INT32_MAX) slot = static_cast<int32_t>(at);
@@ -124,20 +155,26 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const __grid_constant__ P
     }
 }
 
-std::atomic<uint64_t> configured{0};
+template <int THREADS>
+cudaError_t launch(const PlanParams &p, cudaStream_t s)
+{
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(plan_kernel<THREADS>, 16 * (PLAN_MAX_REQUESTS + 1), done);
+    if (e != cudaSuccess) return e;
+    // a CTA for every token a thread, one an SM at most: each repeats the prefix sums
+    int64_t grid = (p.tokens + THREADS - 1) / THREADS;
+    const int64_t cap = sm_count();
+    grid = grid < 1 ? 1 : (grid > cap ? cap : grid);
+    plan_kernel<THREADS><<<static_cast<unsigned>(grid), THREADS, 16 * (p.requests + 1), s>>>(p);
+    return cudaGetLastError();
+}
 
 }  // namespace
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t s)
 {
-    const int smem = 4 * (3 * p.requests + 2);
-    cudaError_t e = allow_smem(plan_kernel, 4 * (3 * PLAN_MAX_REQUESTS + 2), configured);
-    if (e != cudaSuccess) return e;
-    // a CTA for every 4096 tokens (four a thread), 64 at most: each repeats the prefix sums
-    int64_t grid = (p.tokens + 4 * THREADS - 1) / (4 * THREADS);
-    grid = grid < 1 ? 1 : (grid > 64 ? 64 : grid);
-    plan_kernel<<<static_cast<unsigned>(grid), THREADS, smem, s>>>(p);
-    return cudaGetLastError();
+    // small CTAs start and synchronise faster; a thread then has up to four requests
+    return p.requests <= 1024 ? launch<256>(p, s) : launch<1024>(p, s);
 }
 
 }  // namespace st

@@ -5,7 +5,7 @@
 
 namespace st {
 
-constexpr int PLAN_MAX_REQUESTS = 16384;  // three prefix arrays in one CTA's shared memory
+constexpr int PLAN_MAX_REQUESTS = 8192;  // four arrays in one CTA's shared memory
 
 struct PlanParams {
     const int32_t *lens, *new_tokens, *free_pages, *free_count;

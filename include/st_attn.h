@@ -448,10 +448,10 @@ typedef struct {
  *   slots, positions [tokens]: of each token; -1 for tokens of a request not served and for entries
  *              past the last token (and the slot of a token whose block table entry is negative)
  *   status     [requests]: 0 served, 1 not served
- * Inputs and outputs must not overlap (block_table apart).  requests: 1 .. 16384; tokens: 1 .. 2^30;
+ * Inputs and outputs must not overlap (block_table apart).  requests: 1 .. 8192; tokens: 1 .. 2^30;
  * page_size: 1 .. 2^20; max_pages: 1 .. 2^24.  Slots are 32-bit: a slot past 2^31 - 1 is given as -1.
  * Errors: ST_ERR_INVALID_ARG (NULL pointer, sizes, an output that is an input), ST_ERR_UNSUPPORTED
- * (requests > 16384), ST_ERR_CUDA. */
+ * (requests > 8192), ST_ERR_CUDA. */
 typedef struct {
     int64_t requests, tokens, max_pages, table_stride, page_size, free_capacity;
 } st_plan_desc_t;
@@ -478,7 +478,7 @@ ST_API st_status_t st_paged_append(const void *q, const void *k, const void *v, 
  * of length 0 gets O = 0, lse = -inf.  A key whose page is outside 0 .. num_pages - 1 is not seen, and
  * the window's error word records it (ST_ERR_BAD_PAGE from st_window_check).  Cache rows that are
  * not seen are not used, whatever they hold.  d: 64 or 128; dtype: ST_BF16 or ST_FP16; heads / kv_heads
- * <= 64; page_size a multiple of 16.  The order of the sums depends on lens and on the device
+ * <= 64; requests <= 8192; page_size a multiple of 16.  The order of the sums depends on lens and on the device
  * only: the same inputs give the same bits.
  * Errors: ST_ERR_INVALID_ARG, ST_ERR_UNSUPPORTED, ST_ERR_ALIGNMENT, ST_ERR_NOT_UPLOADED,
  * ST_ERR_WORKSPACE, ST_ERR_CUDA. */
