@@ -30,15 +30,18 @@ _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 class _On:
     """The inputs' device made current for the call, and the stream to launch on."""
 
+    __slots__ = ("guard", "stream")
+
     def __init__(self, device, stream):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        index = device.index
+        self.guard = None if index == torch._C._cuda_getDevice() else torch.cuda.device(device)
         if stream is None:
-            stream = torch.cuda.current_stream(device).cuda_stream
+            stream = torch._C._cuda_getCurrentRawStream(index)
         elif isinstance(stream, torch.cuda.Stream):
             if stream.device != device:
                 raise ValueError("the stream belongs to another device than the tensors")
             stream = stream.cuda_stream
-        self.stream = _c.c_void_p(int(stream))
+        self.stream = int(stream)
 
     def __enter__(self):
         if self.guard is not None:
@@ -60,9 +63,9 @@ def _check(name, t, shape, dtype, device):
     """A CUDA tensor of this shape, type and device whose rows are contiguous."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {device}, not {tuple(t.shape)} {t.dtype} on {t.device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
@@ -73,12 +76,14 @@ def _check_flat(name, t, shape, dtype, device):
 
 
 def _strides(t):
-    return _abi.st_strides_t(t.stride(0), t.stride(1), t.stride(2))
+    s = t.stride()
+    return _abi.st_strides_t(s[0], s[1], s[2])
 
 
 def _token_strides(t):
     """[tokens, heads, d] as [1, heads, tokens, d]."""
-    return _abi.st_strides_t(0, t.stride(1), t.stride(0))
+    s = t.stride()
+    return _abi.st_strides_t(0, s[1], s[0])
 
 
 def _p(t):
