@@ -21,6 +21,8 @@
 // dealt out in turns (there and back), longest first; no counter, so no memory to clear and the same
 // order every time.  Per 128 x 128 tile the tensor core needs 1024 cycles at d = 128 and the
 // exponentials 1024 cycles of the special-function units.
+#include <type_traits>
+
 #include "kernels.h"
 #include "lm.h"
 #include "window_tiles.cuh"
@@ -479,67 +481,73 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
             for (int32_t tile = r.ns > 0 ? 0 : r.kb0;; tile = tile + 1 == r.ns ? r.kb0 : tile + 1) {
                 if (!(ok = wait_all(&bars->s_full[x], nS))) break;
                 const int32_t base = tile * 128;
-                uint32_t kw[4] = {~0u, ~0u, ~0u, ~0u};  // columns this row sees
-                if (!(live && base + 127 <= pos && (p.g.window == 0 || base > pos - p.g.window || base + 128 <= p.g.sinks))) {
-                    const uint64_t b0 = live ? window_bits64(pos, p.g.window, p.g.sinks, base) : 0ull;
-                    const uint64_t b1 = live ? window_bits64(pos, p.g.window, p.g.sinks, base + 64) : 0ull;
-                    kw[0] = static_cast<uint32_t>(b0);
-                    kw[1] = static_cast<uint32_t>(b0 >> 32);
-                    kw[2] = static_cast<uint32_t>(b1);
-                    kw[3] = static_cast<uint32_t>(b1 >> 32);
-                }
-                auto mask = [&](uint32_t (&v)[32], uint32_t keep) {
-                    if (__all_sync(0xffffffffu, keep == ~0u)) return;  // (the warp stays together)
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] = (keep & (1u << c)) ? v[c] : 0xFF800000u;
-                };
+                const bool whole = live && base + 127 <= pos && (p.g.window == 0 || base > pos - p.g.window || base + 128 <= p.g.sinks);
                 // The exponentials of a 32-column piece are taken with the maximum so far while the next
                 // pieces load and their maxima are found: once the last piece is in registers the tile's
                 // maximum is known, and if it is more than 2^8 larger (or the first), the tile is read
                 // again with the new one.  Until then nothing has overwritten it.
                 float alpha = 1.f, ps[4];
                 uint32_t v0[32], v1[32], v2[32], pk[32];
-                bool seek = __any_sync(0xffffffffu, m == -INFINITY);
-                for (;;) {
-                    float mt = -INFINITY;
-                    if (seek) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            tmem_ld32(tS + 32 * c, v0);
-                            tmem_wait_ld();
-                            mask(v0, kw[c]);
-                            mt = fmaxf(mt, max32(v0));
-                        }
-                        const float m_new = fmaxf(m, mt * sc);
-                        if (m_new > m + RESCALE_LOG2) {  // also the first finite maximum
-                            alpha *= ex2(m - m_new);
-                            m = m_new;
-                        }
-                        mt = -INFINITY;
+                auto first_half = [&](auto masked) {
+                    uint32_t kw[4];  // columns this row sees
+                    if constexpr (decltype(masked)::value) {
+                        const uint64_t b0 = live ? window_bits64(pos, p.g.window, p.g.sinks, base) : 0ull;
+                        const uint64_t b1 = live ? window_bits64(pos, p.g.window, p.g.sinks, base + 64) : 0ull;
+                        kw[0] = static_cast<uint32_t>(b0);
+                        kw[1] = static_cast<uint32_t>(b0 >> 32);
+                        kw[2] = static_cast<uint32_t>(b1);
+                        kw[3] = static_cast<uint32_t>(b1 >> 32);
                     }
-                    const float nb = (m == -INFINITY) ? 0.f : C::BIAS - m;
-                    ps[0] = ps[1] = ps[2] = ps[3] = 0.f;
-                    tmem_ld32(tS, v0);
-                    tmem_wait_ld();
-                    tmem_ld32(tS + 32, v1);
-                    mask(v0, kw[0]);
-                    mt = max32(v0);
-                    tmem_wait_ld();
-                    tmem_ld32(tS + 64, v2);
-                    mask(v1, kw[1]);
-                    mt = fmaxf(mt, max32(v1));
-                    weights<DT>(v0, sc, nb, ps, pk, 0);
-                    tmem_wait_ld();
-                    tmem_ld32(tS + 96, v0);
-                    mask(v2, kw[2]);
-                    mt = fmaxf(mt, max32(v2));
-                    weights<DT>(v1, sc, nb, ps, pk, 16);
-                    tmem_wait_ld();
-                    mask(v0, kw[3]);
-                    mt = fmaxf(mt, max32(v0));
-                    if (!__any_sync(0xffffffffu, mt * sc > m + RESCALE_LOG2)) break;
-                    seek = true;
-                }
+                    auto mask = [&](uint32_t (&v)[32], int c) {
+                        if constexpr (decltype(masked)::value) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = (kw[c] & (1u << e)) ? v[e] : 0xFF800000u;
+                        }
+                    };
+                    bool seek = __any_sync(0xffffffffu, m == -INFINITY);
+                    for (;;) {
+                        float mt = -INFINITY;
+                        if (seek) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                tmem_ld32(tS + 32 * c, v0);
+                                tmem_wait_ld();
+                                mask(v0, c);
+                                mt = fmaxf(mt, max32(v0));
+                            }
+                            const float m_new = fmaxf(m, mt * sc);
+                            if (m_new > m + RESCALE_LOG2) {  // also the first finite maximum
+                                alpha *= ex2(m - m_new);
+                                m = m_new;
+                            }
+                        }
+                        const float nb = (m == -INFINITY) ? 0.f : C::BIAS - m;
+                        ps[0] = ps[1] = ps[2] = ps[3] = 0.f;
+                        tmem_ld32(tS, v0);
+                        tmem_wait_ld();
+                        tmem_ld32(tS + 32, v1);
+                        mask(v0, 0);
+                        mt = max32(v0);
+                        tmem_wait_ld();
+                        tmem_ld32(tS + 64, v2);
+                        mask(v1, 1);
+                        mt = fmaxf(mt, max32(v1));
+                        weights<DT>(v0, sc, nb, ps, pk, 0);
+                        tmem_wait_ld();
+                        tmem_ld32(tS + 96, v0);
+                        mask(v2, 2);
+                        mt = fmaxf(mt, max32(v2));
+                        weights<DT>(v1, sc, nb, ps, pk, 16);
+                        tmem_wait_ld();
+                        mask(v0, 3);
+                        mt = fmaxf(mt, max32(v0));
+                        if (!__any_sync(0xffffffffu, mt * sc > m + RESCALE_LOG2)) break;
+                        seek = true;
+                    }
+                };
+                // (one straight piece of code for the tiles that need no mask, three in four and more)
+                if (__all_sync(0xffffffffu, whole)) first_half(std::false_type());
+                else first_half(std::true_type());
                 if (C::OWN_P) {  // S is no longer needed
                     tc_fence_before();
                     __syncwarp();
