@@ -40,6 +40,26 @@ inline st_status_t check_strides(const st_strides_t &s, int64_t batch, int64_t h
     return ST_OK;
 }
 
+// Whether one of the outputs starts where an input or another output does: it would be overwritten
+// while it is still read.  (Overlaps beyond that cannot be told from interleaved views.)
+template <int NOUT, int NIN>
+bool same_start(const void *const (&outs)[NOUT], const void *const (&ins)[NIN])
+{
+    for (int i = 0; i < NOUT; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (outs[i] == outs[j]) return true;
+        for (int j = 0; j < NIN; ++j)
+            if (outs[i] == ins[j]) return true;
+    }
+    return false;
+}
+
+// Same layout of a [batch, heads, rows, width] tensor.
+inline bool same_strides(const st_strides_t &a, const st_strides_t &b, int64_t batch, int64_t heads, int64_t rows)
+{
+    return (batch == 1 || a.batch == b.batch) && (heads == 1 || a.head == b.head) && (rows == 1 || a.row == b.row);
+}
+
 inline st_status_t check_window(const st_window_t *w)
 {
     if (!w) return ST_ERR_INVALID_ARG;

@@ -180,6 +180,10 @@ st_status_t st_qk_norm_rope(const void *q, const void *k, const void *wq, const 
     if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(q_out, 16) || !aligned_to(k_out, 16) ||
         !aligned_to(wq, 16) || !aligned_to(wk, 16) || !aligned_to(turns, 8) || !aligned_to(positions, 4))
         return ST_ERR_ALIGNMENT;
+    if (st::same_start<2, 4>({q_out, k_out}, {wq, wk, turns, positions}) || q_out == k || k_out == q ||
+        (q_out == q && !st::same_strides(desc->q_out, desc->q, desc->batch, desc->heads, desc->n)) ||
+        (k_out == k && !st::same_strides(desc->k_out, desc->k, desc->batch, desc->kv_heads, desc->n)))
+        return ST_ERR_INVALID_ARG;
     const int es = elem_bytes(desc->dtype);
     st::RopeParams p = rope_params(desc, wq, wk, turns, positions);
     p.q = tensor(q, desc->q, es);
@@ -215,7 +219,13 @@ st_status_t st_qk_norm_rope_bwd(const void *q, const void *k, const void *gq, co
     if (wq) {
         if (!workspace || workspace_bytes < st_qk_norm_rope_bwd_workspace_bytes(desc)) return ST_ERR_WORKSPACE;
         if (!aligned_to(workspace, 256)) return ST_ERR_ALIGNMENT;
+        if (st::same_start<3, 10>({dwq, dwk, workspace}, {q, k, gq, gk, wq, wk, turns, positions, dq, dk}))
+            return ST_ERR_INVALID_ARG;
     }
+    if (st::same_start<2, 6>({dq, dk}, {q, k, wq, wk, turns, positions}) || dq == gk || dk == gq ||
+        (dq == gq && !st::same_strides(desc->dq, desc->q_out, desc->batch, desc->heads, desc->n)) ||
+        (dk == gk && !st::same_strides(desc->dk, desc->k_out, desc->batch, desc->kv_heads, desc->n)))
+        return ST_ERR_INVALID_ARG;
     const int es = elem_bytes(desc->dtype);
     st::RopeParams p = rope_params(desc, wq, wk, turns, positions);
     p.q = tensor(q, desc->q, es);
@@ -281,6 +291,9 @@ st_status_t st_paged_append(const void *q, const void *k, const void *v, const v
         !aligned_to(k_pages, 16) || !aligned_to(v_pages, 16) || !aligned_to(wq, 16) || !aligned_to(wk, 16) ||
         !aligned_to(turns, 8) || !aligned_to(positions, 4) || !aligned_to(slots, 4))
         return ST_ERR_ALIGNMENT;
+    if (st::same_start<3, 7>({q_out, k_pages, v_pages}, {k, v, wq, wk, turns, positions, slots}) || k_pages == q ||
+        v_pages == q || (q_out == q && !st::same_strides(desc->q_out, desc->q, 1, desc->heads, desc->n)))
+        return ST_ERR_INVALID_ARG;
     st::RopeParams p = rope_params(desc, wq, wk, turns, positions);
     p.q = tensor(q, desc->q, es);
     p.k = tensor(k, desc->k, es);
@@ -339,6 +352,7 @@ st_status_t st_paged_decode(const void *q, const void *k_pages, const void *v_pa
     if ((cs = st::check_window(w)) != ST_OK) return cs;
     if (!workspace || workspace_bytes < st_paged_decode_workspace_bytes(desc, w)) return ST_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return ST_ERR_ALIGNMENT;
+    if (st::same_start<3, 5>({o, lse, workspace}, {q, k_pages, v_pages, block_table, lens})) return ST_ERR_INVALID_ARG;
     st::PagedParams p;
     memset(&p, 0, sizeof(p));
     p.q = q;

@@ -125,6 +125,7 @@ st_status_t st_window_fwd(const void *q, const void *k, const void *v, const int
         !aligned_to(lens, 4))
         return ST_ERR_ALIGNMENT;
     if ((cs = st::check_window(w)) != ST_OK) return cs;
+    if (st::same_start<2, 4>({o, lse}, {q, k, v, lens})) return ST_ERR_INVALID_ARG;
     if (!st::encode_fn()) return ST_ERR_CUDA;
     st::WindowFwdParams p;
     memset(&p, 0, sizeof(p));
@@ -176,6 +177,7 @@ st_status_t st_window_bwd(const void *q, const void *k, const void *v, const voi
         return ST_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < z.total()) return ST_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return ST_ERR_ALIGNMENT;
+    if (st::same_start<4, 7>({dq, dk, dv, workspace}, {q, k, v, o, lse, dO, lens})) return ST_ERR_INVALID_ARG;
     if (!st::encode_fn()) return ST_ERR_CUDA;
     if (!make_map(&p.q, q, desc->q, desc, w->heads, desc->nq) || !make_map(&p.k, k, desc->k, desc, w->kv_heads, desc->nk) ||
         !make_map(&p.v, v, desc->v, desc, w->kv_heads, desc->nk) || !make_map(&p.dout, dO, desc->dout, desc, w->heads, desc->nq))

@@ -3,7 +3,8 @@ and keys with the position rotation, and a paged key/value cache.
 
 The bindings of the second half of include/st_attn.h, same names; they marshal tensors (with their
 strides) into the C calls.  As elsewhere in the package there is no CPU path.  Calls are
-asynchronous on ``stream`` (default: the current stream of the inputs' device).
+asynchronous on ``stream`` (default: the current stream of the inputs' device); what they return is
+allocated for that stream.
 
     win = WindowLayout(heads=16, kv_heads=4, window=1024, sinks=16).upload()
     rope = RopeTable(128, scaling="yarn", factor=16, original=8192, device="cuda")
@@ -20,6 +21,7 @@ from __future__ import annotations
 import ctypes as _c
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _abi
 
@@ -28,20 +30,26 @@ _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 class _On:
-    """The inputs' device made current for the call, and the stream to launch on."""
+    """The inputs' device made current for the call, and the stream to launch on.  What a call
+    allocates (outputs, workspaces) is allocated inside, so it belongs to that stream too: memory
+    that another stream has yet to finish with is not handed out, and a workspace dropped at the end
+    of the call is reused behind the kernels that read it."""
 
     __slots__ = ("guard", "stream")
 
     def __init__(self, device, stream):
         index = device.index
-        self.guard = None if index == torch._C._cuda_getDevice() else torch.cuda.device(device)
         if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(index)
-        elif isinstance(stream, torch.cuda.Stream):
-            if stream.device != device:
-                raise ValueError("the stream belongs to another device than the tensors")
-            stream = stream.cuda_stream
-        self.stream = int(stream)
+            self.guard = None if index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+            self.stream = torch._C._cuda_getCurrentRawStream(index)
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            raw = int(stream)
+            stream = torch.cuda.ExternalStream(raw, device) if raw else torch.cuda.default_stream(device)
+        elif stream.device != device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        self.guard = torch.cuda.stream(stream)
+        self.stream = stream.cuda_stream
 
     def __enter__(self):
         if self.guard is not None:
@@ -167,14 +175,14 @@ def st_window_fwd(q, k, v, layout: WindowLayout, q_start=None, lens=None, o=None
     lengths of a padded batch; rows and keys at lens[b] and beyond are padding (O = 0, lse = -inf).
     Asynchronous: ``layout.check()`` or ``check=True`` reports a device wait that ran out."""
     desc = _window_desc(q, k, v, layout, q_start, lens)
-    if o is None:
-        o = torch.empty_like(q)
-    _check("o", o, q.shape, q.dtype, q.device)
-    if lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    _check_flat("lse", lse, q.shape[:3], torch.float32, q.device)
-    desc.o = _strides(o)
     with _On(q.device, stream) as s:
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        _check("o", o, q.shape, q.dtype, q.device)
+        _check_flat("lse", lse, q.shape[:3], torch.float32, q.device)
+        desc.o = _strides(o)
         _abi.check(layout._lib.st_window_fwd(_p(q), _p(k), _p(v), _p(lens), layout.handle, _p(o), _p(lse),
                                              _c.byref(desc), s), "st_window_fwd")
     if check:
@@ -192,15 +200,15 @@ def st_window_bwd(q, k, v, o, lse, do, layout: WindowLayout, q_start=None, lens=
                   workspace=None, stream=None, check=False):
     """dQ, dK, dV of st_window_fwd (recomputing P from the saved lse); deterministic."""
     desc = _window_desc(q, k, v, layout, q_start, lens)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    for name, t, like in (("o", o, q), ("do", do, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _check(name, t, like.shape, q.dtype, q.device)
-    _check_flat("lse", lse, q.shape[:3], torch.float32, q.device)
-    desc.o, desc.dout = _strides(o), _strides(do)
-    desc.dq, desc.dk, desc.dv = _strides(dq), _strides(dk), _strides(dv)
     with _On(q.device, stream) as s:
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        for name, t, like in (("o", o, q), ("do", do, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+            _check(name, t, like.shape, q.dtype, q.device)
+        _check_flat("lse", lse, q.shape[:3], torch.float32, q.device)
+        desc.o, desc.dout = _strides(o), _strides(do)
+        desc.dq, desc.dk, desc.dv = _strides(dq), _strides(dk), _strides(dv)
         need = layout._lib.st_window_bwd_workspace_bytes(_c.byref(desc), layout.handle)
         workspace = _workspace(workspace, need, q.device)
         _abi.check(layout._lib.st_window_bwd(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(do), _p(lens), layout.handle,
@@ -209,10 +217,6 @@ def st_window_bwd(q, k, v, o, lse, do, layout: WindowLayout, q_start=None, lens=
     if check:
         layout.check(stream)
     return dq, dk, dv
-
-
-def _rows(t):
-    return t if t.shape[-1] == 1 or t.stride(-1) == 1 else t.contiguous()
 
 
 def _as_rows(t):
@@ -239,6 +243,7 @@ class WindowAttention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, lens = ctx.saved_tensors
         dq, dk, dv = st_window_bwd(q, k, v, o, lse, _as_rows(do), ctx.layout, q_start=ctx.q_start, lens=lens)
@@ -306,12 +311,12 @@ def st_qk_norm_rope(q, k, rope: RopeTable, wq=None, wk=None, eps: float = 1e-6, 
     rotation, in one pass; returns (q_out, k_out), contiguous unless given (q_out may be q).
     Positions are positions ([n] or [B, n] int32), or start, start + 1, ..."""
     desc = _rope_desc(q, k, rope, wq, wk, eps, positions, start, False)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-    _check("q_out", q_out, q.shape, q.dtype, q.device)
-    _check("k_out", k_out, k.shape, q.dtype, q.device)
-    desc.q_out, desc.k_out = _strides(q_out), _strides(k_out)
     with _On(q.device, stream) as s:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+        _check("q_out", q_out, q.shape, q.dtype, q.device)
+        _check("k_out", k_out, k.shape, q.dtype, q.device)
+        desc.q_out, desc.k_out = _strides(q_out), _strides(k_out)
         _abi.check(_abi.load().st_qk_norm_rope(_p(q), _p(k), _p(wq), _p(wk), _p(rope.turns), _p(positions), _p(q_out),
                                                _p(k_out), _c.byref(desc), s), "st_qk_norm_rope")
     return q_out, k_out
@@ -331,13 +336,13 @@ def st_qk_norm_rope_bwd(q, k, gq, gk, rope: RopeTable, wq=None, wk=None, eps: fl
     """Gradients (dq, dk, dwq, dwk) for the output gradients gq, gk; dwq and dwk are fp32, or None
     without weights.  dq may be gq and dk may be gk."""
     desc = _rope_desc(q, k, rope, wq, wk, eps, positions, start, False)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    for name, t, like in (("gq", gq, q), ("gk", gk, k), ("dq", dq, q), ("dk", dk, k)):
-        _check(name, t, like.shape, q.dtype, q.device)
-    desc.q_out, desc.k_out, desc.dq, desc.dk = _strides(gq), _strides(gk), _strides(dq), _strides(dk)
     dwq = dwk = None
     with _On(q.device, stream) as s:
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        for name, t, like in (("gq", gq, q), ("gk", gk, k), ("dq", dq, q), ("dk", dk, k)):
+            _check(name, t, like.shape, q.dtype, q.device)
+        desc.q_out, desc.k_out, desc.dq, desc.dk = _strides(gq), _strides(gk), _strides(dq), _strides(dk)
         if wq is not None:
             dw = torch.empty((2, q.shape[-1]), dtype=torch.float32, device=q.device)
             dwq, dwk = dw[0], dw[1]
@@ -359,6 +364,7 @@ class QKNormRope(torch.autograd.Function):
         return st_qk_norm_rope(q, k, rope, wq=wq, wk=wk, eps=eps, positions=positions, start=start)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gq, gk):
         q, k, wq, wk, positions = ctx.saved_tensors
         dq, dk, dwq, dwk = st_qk_norm_rope_bwd(q, k, _as_rows(gq), _as_rows(gk), ctx.rope, wq=wq, wk=wk, eps=ctx.eps,
@@ -401,12 +407,12 @@ def st_paged_plan(lens, new, block_table, free_pages, free_count, page_size: int
     _check("block_table", block_table, (R, block_table.shape[1]), i32, device)
     _check_flat("free_pages", free_pages, free_pages.shape, i32, device)
     _check_flat("free_count", free_count, (1,), i32, device)
-    if plan is None:
-        plan = PagedPlan(R, tokens, device)
-    elif plan.requests != R or plan.tokens != tokens or plan.device != device:
-        raise ValueError("plan was made for other sizes or another device")
     desc = _abi.st_plan_desc_t(R, tokens, block_table.shape[1], block_table.stride(0), page_size, free_pages.shape[0])
     with _On(device, stream) as s:
+        if plan is None:
+            plan = PagedPlan(R, tokens, device)
+        elif plan.requests != R or plan.tokens != tokens or plan.device != device:
+            raise ValueError("plan was made for other sizes or another device")
         _abi.check(_abi.load().st_paged_plan(_p(lens), _p(new), _p(block_table), _p(free_pages), _p(free_count),
                                              _p(plan.lens), _p(plan.free_left), _p(plan.offsets), _p(plan.slots),
                                              _p(plan.positions), _p(plan.status), _c.byref(desc), s), "st_paged_plan")
@@ -434,11 +440,11 @@ def st_paged_append(q, k, v, rope: RopeTable, slots, positions, k_pages, v_pages
     if positions is None or positions.dim() != 1:
         raise ValueError("positions must be [tokens]")
     pages = _pages(k_pages, v_pages, KV, d, q.dtype, q.device)
-    q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    _check("q_out", q_out, q.shape, q.dtype, q.device)
-    desc.q_out = _token_strides(q_out)
     vs = _token_strides(v)
     with _On(q.device, stream) as s:
+        q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        _check("q_out", q_out, q.shape, q.dtype, q.device)
+        desc.q_out = _token_strides(q_out)
         _abi.check(_abi.load().st_paged_append(_p(q), _p(k), _p(v), _p(wq), _p(wk), _p(rope.turns), _p(positions),
                                                _p(slots), _p(q_out), _p(k_pages), _p(v_pages), _c.byref(vs),
                                                _c.byref(pages), _c.byref(desc), s), "st_paged_append")
@@ -466,12 +472,12 @@ def st_paged_decode(q, k_pages, v_pages, block_table, lens, layout: WindowLayout
     pages = _pages(k_pages, v_pages, layout.kv_heads, d, q.dtype, q.device)
     _check("block_table", block_table, (R, block_table.shape[1]), torch.int32, q.device)
     _check_flat("lens", lens, (R,), torch.int32, q.device)
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((R, H), dtype=torch.float32, device=q.device) if lse is None else lse
-    _check_flat("o", o, q.shape, q.dtype, q.device)
-    _check_flat("lse", lse, (R, H), torch.float32, q.device)
     desc = _abi.st_paged_desc_t(R, d, block_table.shape[1], block_table.stride(0), _dtype(q), 0, pages)
     with _On(q.device, stream) as s:
+        o = torch.empty_like(q) if o is None else o
+        lse = torch.empty((R, H), dtype=torch.float32, device=q.device) if lse is None else lse
+        _check_flat("o", o, q.shape, q.dtype, q.device)
+        _check_flat("lse", lse, (R, H), torch.float32, q.device)
         if workspace is None:
             need = layout._lib.st_paged_decode_workspace_bytes(_c.byref(desc), layout.handle)
         workspace = _workspace(workspace, need if workspace is None else 0, q.device)

@@ -354,10 +354,12 @@ typedef struct {
  *   lens  device int32 [batch] or NULL: the sequence of batch element b has lens[b] positions
  *         (clamped to 0 .. nk; NULL: nk).  Rows at positions lens[b] and beyond are padding: O = 0
  *         and lse = -inf; keys there are not seen, whatever they hold (NaN included).
+ * o and lse must not overlap each other or an input.
  * A NaN or an infinity in a row before lens[b] may reach any row of its batch element and group.
  * 16-bit products with fp32 accumulation; the probabilities are rounded to the inputs' type for
  * the second product.
- * Errors: ST_ERR_INVALID_ARG (NULL pointer, sizes, q_start < 0, another device current),
+ * Errors: ST_ERR_INVALID_ARG (NULL pointer, sizes, q_start < 0, another device current, an output that
+ * is another array),
  * ST_ERR_UNSUPPORTED, ST_ERR_ALIGNMENT, ST_ERR_NOT_UPLOADED, ST_ERR_CUDA. */
 ST_API st_status_t st_window_fwd(const void *q, const void *k, const void *v, const int32_t *lens,
                                  const st_window_t *window, void *o, float *lse,
@@ -367,6 +369,7 @@ ST_API st_status_t st_window_fwd(const void *q, const void *k, const void *v, co
  * padding rows and unseen keys get 0, whatever dO, O and lse hold there).  The sums run in a fixed
  * order: the same inputs give the same bits.  dS (and P) are rounded to the inputs' type for their
  * products; with ST_FP16 they are scaled by powers of two that keep them in range, per key head.
+ * dq, dk, dv and the workspace must not overlap each other or an input.
  * Errors as for the forward, and ST_ERR_WORKSPACE. */
 ST_API size_t st_window_bwd_workspace_bytes(const st_window_desc_t *desc, const st_window_t *window);
 ST_API st_status_t st_window_bwd(const void *q, const void *k, const void *v, const void *o,
@@ -408,14 +411,16 @@ typedef struct {
  * pos = positions[b, t], or start + t when positions is NULL.  Angles are products of 64-bit
  * integers modulo a turn, so far positions keep their accuracy.  fp32 arithmetic, rounded once.  turns:
  * device [rot / 2].
- * q_out may be q and k_out may be k (same strides).  Errors: ST_ERR_INVALID_ARG, ST_ERR_UNSUPPORTED,
+ * q_out may be q and k_out may be k (same strides); otherwise outputs overlap nothing.  Errors:
+ * ST_ERR_INVALID_ARG (NULL pointer, sizes, an output that is another array), ST_ERR_UNSUPPORTED,
  * ST_ERR_ALIGNMENT, ST_ERR_CUDA. */
 ST_API st_status_t st_qk_norm_rope(const void *q, const void *k, const void *wq, const void *wk,
                                    const uint64_t *turns, const int32_t *positions, void *q_out, void *k_out,
                                    const st_rope_desc_t *desc, st_stream_t stream);
 
 /* Gradients: gq, gk of the outputs; dq, dk of the inputs (dq may be gq, dk may be gk, same strides);
- * dwq, dwk: [d] fp32 (NULL without weights), summed in a fixed order. */
+ * dwq, dwk: [d] fp32 (NULL without weights), summed in a fixed order.  Other outputs and the workspace
+ * overlap nothing. */
 ST_API size_t st_qk_norm_rope_bwd_workspace_bytes(const st_rope_desc_t *desc);
 ST_API st_status_t st_qk_norm_rope_bwd(const void *q, const void *k, const void *gq, const void *gk,
                                        const void *wq, const void *wk, const uint64_t *turns,
@@ -465,7 +470,8 @@ ST_API st_status_t st_paged_plan(const int32_t *lens, const int32_t *new_tokens,
  * desc is as for st_qk_norm_rope with batch = 1 and n = tokens (strides: row = token, head; k_out and
  * start unused); v: strides of the values.  positions, slots: [tokens] int32, as st_paged_plan gives
  * them.  A token whose slot is outside 0 .. num_pages * page_size - 1 is skipped: its q_out row and
- * the cache are left as they were.  Slots must be distinct: of two tokens with one slot either may
+ * the cache are left as they were.  q_out may be q (same strides); otherwise outputs overlap nothing.
+ * Slots must be distinct: of two tokens with one slot either may
  * be stored, in part. */
 ST_API st_status_t st_paged_append(const void *q, const void *k, const void *v, const void *wq, const void *wk,
                                    const uint64_t *turns, const int32_t *positions, const int32_t *slots,
@@ -478,7 +484,8 @@ ST_API st_status_t st_paged_append(const void *q, const void *k, const void *v, 
  * of length 0 gets O = 0, lse = -inf.  A key whose page is outside 0 .. num_pages - 1 is not seen, and
  * the window's error word records it (ST_ERR_BAD_PAGE from st_window_check).  Cache rows that are
  * not seen are not used, whatever they hold.  d: 64 or 128; dtype: ST_BF16 or ST_FP16; heads / kv_heads
- * <= 64; requests <= 8192; page_size a multiple of 16.  The order of the sums depends on lens and on the device
+ * <= 64; requests <= 8192; page_size a multiple of 16; max_pages * page_size <= 2^30.  o, lse and the
+ * workspace must not overlap each other or an input.  The order of the sums depends on lens and on the device
  * only: the same inputs give the same bits.
  * Errors: ST_ERR_INVALID_ARG, ST_ERR_UNSUPPORTED, ST_ERR_ALIGNMENT, ST_ERR_NOT_UPLOADED,
  * ST_ERR_WORKSPACE, ST_ERR_CUDA. */

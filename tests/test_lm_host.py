@@ -264,3 +264,36 @@ def test_reference_gradient_against_differences():
             a[i], b[i] = x + 1e-6 * d, x - 1e-6 * d
             num = float((f(*a) - f(*b)) / 2e-6)
             assert float((grads[i][0] * d).sum()) == pytest.approx(num, rel=1e-6, abs=1e-7)
+
+
+def test_rope_refuses_outputs_that_are_other_arrays(lib):
+    """In place means the same layout, and one output is not the other's input."""
+    at = [P + 0x100000 * i for i in range(12)]
+
+    def run(q_out, k_out, wider=None):
+        x = rope_desc()
+        if wider:
+            getattr(x, wider).row = 128
+        return lib.st_qk_norm_rope(at[0], at[1], at[2], at[3], at[4], None, q_out, k_out, c.byref(x), None)
+    for q_out, k_out in ((at[1], at[6]), (at[5], at[0]), (at[5], at[5]), (at[2], at[6]), (at[5], at[4])):
+        assert run(q_out, k_out) == INVALID
+    assert run(at[0], at[6], "q_out") == INVALID
+    assert run(at[5], at[1], "k_out") == INVALID
+
+    def bwd(dq=at[5], dk=at[6], dwq=at[7], dwk=at[8], ws=at[9]):
+        x = rope_desc()
+        return lib.st_qk_norm_rope_bwd(at[0], at[1], at[10], at[11], at[2], at[3], at[4], None, dq, dk, dwq, dwk, ws, 1 << 30,
+                                       c.byref(x), None)
+    for kw in ({"dq": at[0]}, {"dk": at[1]}, {"dq": at[11]}, {"dk": at[10]}, {"dq": at[6]}, {"dwq": at[8]}, {"dwk": at[5]},
+               {"ws": at[10]}, {"ws": at[7]}):
+        assert bwd(**kw) == INVALID, kw
+
+
+def test_append_refuses_outputs_that_are_other_arrays(lib):
+    at = [P + 0x100000 * i for i in range(12)]
+    s = _abi.st_strides_t(2 * 16 * 64, 16 * 64, 64)
+    g, vs = _abi.st_pages_t(5, 16, s, s), strides(1, 2, 10, 64)
+    for q_out, kp, vp in ((at[1], at[9], at[10]), (at[8], at[9], at[9]), (at[8], at[8], at[10]), (at[8], at[0], at[10]),
+                          (at[8], at[1], at[10]), (at[8], at[9], at[2]), (at[6], at[9], at[10])):
+        assert lib.st_paged_append(at[0], at[1], at[2], at[3], at[4], at[5], at[6], at[7], q_out, kp, vp, c.byref(vs),
+                                   c.byref(g), c.byref(rope_desc(B=1)), None) == INVALID

@@ -323,3 +323,48 @@ def test_serving_steps():
                 assert ((lse[i].to(F64) - ref[1][0, :, 0]).abs() <= 1e-5).all()
     assert lens.tolist() == [len(x) for x in said]
     assert int(count) == P - sum(-(-len(x) // page) for x in said)
+
+
+def test_append_on_a_given_stream():
+    """The zeros of a q_out made by the call come before its rows, whatever the current stream does."""
+    H, KV, d, page, n = 4, 2, 64, 16, 20
+    g = torch.Generator(device="cuda").manual_seed(30)
+    q, k, v = (torch.randn(n, h, d, generator=g, device="cuda").bfloat16() for h in (H, KV, KV))
+    t = bsf.RopeTable(d, device="cuda")
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    slots[3] = -1
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    kp, vp = (torch.zeros(2, KV, page, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    want = bsf.st_paged_append(q, k, v, t, slots, pos, kp, vp)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)  # the current stream is busy
+    got = bsf.st_paged_append(q, k, v, t, slots, pos, kp, vp, stream=s)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and (got[3] == 0).all() and (got[4] != 0).any()
+
+
+def test_append_in_place():
+    H, KV, d, page, n = 4, 2, 128, 16, 33
+    g = torch.Generator(device="cuda").manual_seed(31)
+    q, k, v = (torch.randn(n, h, d, generator=g, device="cuda").bfloat16() for h in (H, KV, KV))
+    wq, wk = (1 + 0.1 * torch.randn(d, generator=g, device="cuda") for _ in range(2))
+    t = bsf.RopeTable(64, interleaved=True, device="cuda")
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    kp, vp = (torch.zeros(3, KV, page, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    slots[5] = -1
+    want = bsf.st_paged_append(q, k, v, t, slots, slots, kp, vp, wq=wq, wk=wk)
+    q5 = q[5].clone()
+    bsf.st_paged_append(q, k, v, t, slots, slots, kp, vp, wq=wq, wk=wk, q_out=q)
+    assert torch.equal(q[5], q5)
+    want[5] = q5
+    assert torch.equal(q, want)
+
+
+def test_decode_refuses_outputs_that_are_inputs():
+    kp, vp, table, ln = cache((20, 3), 2, 64, 16, "bf16", seed=32)
+    q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+    lay = bsf.WindowLayout(4, 2, 0, 0).upload()
+    with pytest.raises(bsf.StError):
+        bsf.st_paged_decode(q, kp, vp, table, ln, lay, o=q)

@@ -305,3 +305,52 @@ def test_binding_refusals():
     o, lse = bsf.st_window_fwd(q, k, v, lay)
     with pytest.raises(bsf.StError):
         bsf.st_window_bwd(q, k, v, o, lse, do, lay, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_refuses_outputs_that_are_inputs():
+    q, k, v, do = inputs(1, 4, 4, 130, 130, 64, torch.bfloat16, seed=21)
+    lay = bsf.WindowLayout(4, 4, 64, 2).upload()
+    o, lse = bsf.st_window_fwd(q, k, v, lay)
+    kept = [t.clone() for t in (q, k, v, o, do)]
+    for call in (lambda: bsf.st_window_fwd(q, k, v, lay, o=q), lambda: bsf.st_window_fwd(q, k, v, lay, o=v),
+                 lambda: bsf.st_window_bwd(q, k, v, o, lse, do, lay, dq=do), lambda: bsf.st_window_bwd(q, k, v, o, lse, do, lay, dk=k),
+                 lambda: bsf.st_window_bwd(q, k, v, o, lse, do, lay, dk=o, dv=torch.empty_like(v)),
+                 lambda: bsf.st_window_bwd(q, k, v, o, lse, do, lay, dq=kept[0], dv=kept[0])):
+        with pytest.raises(bsf.StError):
+            call()
+    torch.cuda.synchronize()
+    assert torch.equal(q, kept[0]) and all(torch.equal(a, b) for a, b in zip((k, v, o, do), kept[1:]))
+
+
+def test_given_stream_owns_what_the_call_allocates():
+    """On a stream given by hand that runs behind the current one, the call's workspace stays its own:
+    the current stream's next allocation of that size must not be it."""
+    x = inputs(1, 4, 2, 900, 900, 64, torch.bfloat16, seed=22)
+    lay = bsf.WindowLayout(4, 2, 0, 0).upload()
+    o, lse = bsf.st_window_fwd(*x[:3], lay)
+    want = bsf.st_window_bwd(*x[:3], o, lse, x[3], lay)
+    need = bsf.st_window_bwd_workspace_bytes(x[0], x[1], lay)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    got = bsf.st_window_bwd(*x[:3], o, lse, x[3], lay, stream=s)
+    spoil = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for _ in range(20):
+        spoil[0].fill_(255)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    raw = bsf.st_window_bwd(*x[:3], o, lse, x[3], lay, stream=s.cuda_stream)  # the stream as a number
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(raw, want))
+
+
+def test_no_second_derivative():
+    q, k, v, _ = inputs(1, 4, 2, 40, 40, 64, torch.bfloat16, seed=23)
+    q.requires_grad_()
+    o = bsf.WindowAttention.apply(q, k, v, bsf.WindowLayout(4, 2, 0, 0).upload())
+    gq, = torch.autograd.grad(o.float().sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError):
+        gq.float().sum().backward()
