@@ -16,6 +16,12 @@ __host__ __device__ constexpr uint32_t idesc16(int M, int N, bool a_mn, bool b_m
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Expect more bytes in the current phase, without arriving.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 // One 128-row tile of D columns by TMA (boxes of 64 columns), at row `row` of (head, batch).
 template <int D>
 __device__ __forceinline__ void tma_tile(const CUtensorMap *m, uint8_t *dst, uint64_t *bar, int32_t row, int32_t head, int32_t batch)
