@@ -19,6 +19,7 @@ allocated for that stream.
 from __future__ import annotations
 
 import ctypes as _c
+import struct as _struct
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -37,12 +38,12 @@ class _On:
 
     __slots__ = ("guard", "stream")
 
-    def __init__(self, device, stream):
-        index = device.index
+    def __init__(self, index, stream):
         if stream is None:
-            self.guard = None if index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+            self.guard = None if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
             self.stream = torch._C._cuda_getCurrentRawStream(index)
             return
+        device = torch.device("cuda", index)
         if not isinstance(stream, torch.cuda.Stream):
             raw = int(stream)
             stream = torch.cuda.ExternalStream(raw, device) if raw else torch.cuda.default_stream(device)
@@ -67,41 +68,58 @@ def _dtype(t):
     return _DTYPES[t.dtype]
 
 
-def _check(name, t, shape, dtype, device):
-    """A CUDA tensor of this shape, type and device whose rows are contiguous."""
-    if not t.is_cuda:
+def _strides(name, t, shape, dtype, index):
+    """t's strides, for a CUDA tensor of this shape, type and device whose rows are contiguous."""
+    s = t.stride()
+    if t.shape != shape or t.dtype != dtype or t.get_device() != index or index < 0 or (s and s[-1] != 1 and shape[-1] > 1):
+        _refuse(name, t, shape, dtype, index)
+    return s
+
+
+def _refuse(name, t, shape, dtype, index):
+    if not t.is_cuda or index < 0:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {device}, not {tuple(t.shape)} {t.dtype} on {t.device}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if t.shape != shape or t.dtype != dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on cuda:{index}, not {tuple(t.shape)} {t.dtype} on {t.device}")
+    raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
-def _check_flat(name, t, shape, dtype, device):
-    _check(name, t, shape, dtype, device)
+def _check_flat(name, t, shape, dtype, index):
+    _strides(name, t, shape, dtype, index)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _strides(t):
-    s = t.stride()
-    return _abi.st_strides_t(s[0], s[1], s[2])
+def _by_token(s):
+    """Strides of [tokens, heads, d] as (batch, head, row)."""
+    return 0, s[1], s[0]
 
 
-def _token_strides(t):
-    """[tokens, heads, d] as [1, heads, tokens, d]."""
-    s = t.stride()
-    return _abi.st_strides_t(0, s[1], s[0])
+class _Packer:
+    """Builds a descriptor from a flat list of its fields (several times faster than assigning them)."""
+
+    def __init__(self, cls, fmt):
+        self.cls, self.s = cls, _struct.Struct("=" + fmt)
+        assert self.s.size == _c.sizeof(cls)
+
+    def __call__(self, *fields):
+        return self.cls.from_buffer_copy(self.s.pack(*fields))
+
+
+_window_fields = _Packer(_abi.st_window_desc_t, "5q2i24q")
+_rope_fields = _Packer(_abi.st_rope_desc_t, "7q4i2f18q")
+_paged_fields = _Packer(_abi.st_paged_desc_t, "4q2i8q")
+_NO_STRIDES = (0, 0, 0)
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _workspace(ws, need, device):
+def _workspace(ws, need, like):
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    if not ws.is_cuda or ws.device != device or not ws.is_contiguous():
+        return like.new_empty(need, dtype=torch.uint8) if need else None
+    if ws.get_device() != like.get_device() or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the inputs' device")
     return ws
 
@@ -130,7 +148,7 @@ class WindowLayout:
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
-        with _On(device, stream) as s:
+        with _On(device.index, stream) as s:
             _abi.check(self._lib.st_window_upload(self._h, s), "st_window_upload")
         self.device = device
         return self
@@ -138,7 +156,8 @@ class WindowLayout:
     def check(self, stream=None) -> None:
         """Synchronise and raise StError for a device wait that ran out (ST_ERR_DEVICE_TIMEOUT) or a
         page outside the cache (ST_ERR_BAD_PAGE) since the last check."""
-        with _On(getattr(self, "device", torch.device("cuda", torch.cuda.current_device())), stream) as s:
+        device = getattr(self, "device", None)
+        with _On(torch.cuda.current_device() if device is None else device.index, stream) as s:
             _abi.check(self._lib.st_window_check(self._h, s), "st_window_check")
 
     def __del__(self):
@@ -148,23 +167,24 @@ class WindowLayout:
             h.value = None
 
 
-def _window_desc(q, k, v, layout, q_start, lens):
+def _window_call(q, k, v, layout, q_start, lens):
+    """What a call's tensors agree on: device index, the leading fields of the descriptor, and the
+    strides of q, k and v."""
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("expected [batch, heads, n, d] tensors")
     B, H, nq, d = q.shape
     nk = k.shape[2]
-    _check("q", q, (B, layout.heads, nq, d), q.dtype, q.device)
-    for name, t in (("k", k), ("v", v)):
-        _check(name, t, (B, layout.kv_heads, nk, d), q.dtype, q.device)
+    index, dtype = q.get_device(), q.dtype
+    kshape = (B, layout.kv_heads, nk, d)
+    strides = (_strides("q", q, (B, layout.heads, nq, d), dtype, index)[:3] + _strides("k", k, kshape, dtype, index)[:3] +
+               _strides("v", v, kshape, dtype, index)[:3])
     if lens is not None:
-        _check_flat("lens", lens, (B,), torch.int32, q.device)
+        _check_flat("lens", lens, (B,), torch.int32, index)
     if q_start is None:
         q_start = nk - nq
         if q_start < 0:
             raise ValueError("more queries than keys: give q_start")
-    desc = _abi.st_window_desc_t(B, nq, nk, d, q_start, _dtype(q), 0)
-    desc.q, desc.k, desc.v = _strides(q), _strides(k), _strides(v)
-    return desc
+    return index, (B, nq, nk, d, q_start, _dtype(q), 0), strides
 
 
 def st_window_fwd(q, k, v, layout: WindowLayout, q_start=None, lens=None, o=None, lse=None, stream=None, check=False):
@@ -174,44 +194,45 @@ def st_window_fwd(q, k, v, layout: WindowLayout, q_start=None, lens=None, o=None
     rows).  Row i stands at position q_start + i (default: the last nq of nk).  lens: int32 [B]
     lengths of a padded batch; rows and keys at lens[b] and beyond are padding (O = 0, lse = -inf).
     Asynchronous: ``layout.check()`` or ``check=True`` reports a device wait that ran out."""
-    desc = _window_desc(q, k, v, layout, q_start, lens)
-    with _On(q.device, stream) as s:
+    index, head, strides = _window_call(q, k, v, layout, q_start, lens)
+    with _On(index, stream) as s:
         if o is None:
             o = torch.empty_like(q)
         if lse is None:
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-        _check("o", o, q.shape, q.dtype, q.device)
-        _check_flat("lse", lse, q.shape[:3], torch.float32, q.device)
-        desc.o = _strides(o)
-        _abi.check(layout._lib.st_window_fwd(_p(q), _p(k), _p(v), _p(lens), layout.handle, _p(o), _p(lse),
-                                             _c.byref(desc), s), "st_window_fwd")
+            lse = q.new_empty(q.shape[:3], dtype=torch.float32)
+        else:
+            _check_flat("lse", lse, q.shape[:3], torch.float32, index)
+        desc = _window_fields(*head, *strides, *_strides("o", o, q.shape, q.dtype, index)[:3], *_NO_STRIDES * 4)
+        _abi.check(layout._lib.st_window_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _p(lens), layout._h, o.data_ptr(),
+                                             lse.data_ptr(), _c.byref(desc), s), "st_window_fwd")
     if check:
         layout.check(stream)
     return o, lse
 
 
 def st_window_bwd_workspace_bytes(q, k, layout: WindowLayout, q_start=None) -> int:
-    desc = _window_desc(q, k, k, layout, q_start, None)
-    with _On(q.device, None):
+    index, head, strides = _window_call(q, k, k, layout, q_start, None)
+    desc = _window_fields(*head, *strides, *_NO_STRIDES * 5)
+    with _On(index, None):
         return int(layout._lib.st_window_bwd_workspace_bytes(_c.byref(desc), layout.handle))
 
 
 def st_window_bwd(q, k, v, o, lse, do, layout: WindowLayout, q_start=None, lens=None, dq=None, dk=None, dv=None,
                   workspace=None, stream=None, check=False):
     """dQ, dK, dV of st_window_fwd (recomputing P from the saved lse); deterministic."""
-    desc = _window_desc(q, k, v, layout, q_start, lens)
-    with _On(q.device, stream) as s:
+    index, head, strides = _window_call(q, k, v, layout, q_start, lens)
+    with _On(index, stream) as s:
         dq = torch.empty_like(q) if dq is None else dq
         dk = torch.empty_like(k) if dk is None else dk
         dv = torch.empty_like(v) if dv is None else dv
         for name, t, like in (("o", o, q), ("do", do, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-            _check(name, t, like.shape, q.dtype, q.device)
-        _check_flat("lse", lse, q.shape[:3], torch.float32, q.device)
-        desc.o, desc.dout = _strides(o), _strides(do)
-        desc.dq, desc.dk, desc.dv = _strides(dq), _strides(dk), _strides(dv)
-        need = layout._lib.st_window_bwd_workspace_bytes(_c.byref(desc), layout.handle)
-        workspace = _workspace(workspace, need, q.device)
-        _abi.check(layout._lib.st_window_bwd(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(do), _p(lens), layout.handle,
+            strides += _strides(name, t, like.shape, q.dtype, index)[:3]
+        _check_flat("lse", lse, q.shape[:3], torch.float32, index)
+        desc = _window_fields(*head, *strides)
+        if workspace is None:
+            need = layout._lib.st_window_bwd_workspace_bytes(_c.byref(desc), layout._h)
+        workspace = _workspace(workspace, need if workspace is None else 0, q)
+        _abi.check(layout._lib.st_window_bwd(_p(q), _p(k), _p(v), _p(o), _p(lse), _p(do), _p(lens), layout._h,
                                              _p(dq), _p(dk), _p(dv), _p(workspace), _nbytes(workspace),
                                              _c.byref(desc), s), "st_window_bwd")
     if check:
@@ -270,39 +291,37 @@ class RopeTable:
         self.turns = turns.to(device)
 
 
-def _rope_desc(q, k, rope, wq, wk, eps, positions, start, token_major):
-    """q, k: [B, H, n, d] and [B, KV, n, d], or packed [n, H, d] and [n, KV, d] (token_major)."""
+def _rope_call(q, k, rope, wq, wk, eps, positions, start, token_major):
+    """q, k: [B, H, n, d] and [B, KV, n, d], or packed [n, H, d] and [n, KV, d] (token_major).  Returns
+    the device index, the leading fields of the descriptor, and the strides of q and k."""
     if q.dim() != (3 if token_major else 4) or k.dim() != q.dim():
         raise ValueError("expected [tokens, heads, d] tensors" if token_major else "expected [batch, heads, n, d] tensors")
+    index, dtype = q.get_device(), q.dtype
     if token_major:
         (n, H, d), B, KV = q.shape, 1, k.shape[1]
         kshape = (n, KV, d)
     else:
         (B, H, n, d), KV = q.shape, k.shape[1]
         kshape = (B, KV, n, d)
-    _check("q", q, q.shape, q.dtype, q.device)
-    _check("k", k, kshape, q.dtype, q.device)
+    qs, ks = _strides("q", q, q.shape, dtype, index), _strides("k", k, kshape, dtype, index)
     if (wq is None) != (wk is None):
         raise ValueError("give both norm weights or neither")
     wdt = _dtype(q)
     if wq is not None:
         for name, w in (("wq", wq), ("wk", wk)):
-            _check_flat(name, w, (d,), wq.dtype, q.device)
-        if wq.dtype not in (torch.float32, q.dtype):
+            _check_flat(name, w, (d,), wq.dtype, index)
+        if wq.dtype not in (torch.float32, dtype):
             raise TypeError("norm weights must be fp32 or of the queries' type")
         wdt = _dtype(wq)
-    if rope.turns.device != q.device:
+    if rope.turns.get_device() != index:
         raise ValueError("the rotation table is on another device")
     pos_batch = 0
     if positions is not None:
         shape = (n,) if positions.dim() == 1 else (B, n)
-        _check_flat("positions", positions, shape, torch.int32, q.device)
+        _check_flat("positions", positions, shape, torch.int32, index)
         pos_batch = n if positions.dim() == 2 else 0
-    desc = _abi.st_rope_desc_t(B, H, KV, n, d, start, pos_batch, rope.rot, int(rope.interleaved), _dtype(q), wdt,
-                               eps, rope.mscale)
-    st = _token_strides if token_major else _strides
-    desc.q, desc.k = st(q), st(k)
-    return desc
+    head = (B, H, KV, n, d, start, pos_batch, rope.rot, int(rope.interleaved), _dtype(q), wdt, eps, rope.mscale)
+    return index, head, (_by_token(qs) + _by_token(ks) if token_major else qs[:3] + ks[:3])
 
 
 def st_qk_norm_rope(q, k, rope: RopeTable, wq=None, wk=None, eps: float = 1e-6, positions=None, start: int = 0,
@@ -310,46 +329,45 @@ def st_qk_norm_rope(q, k, rope: RopeTable, wq=None, wk=None, eps: float = 1e-6, 
     """Per-head RMS norm of q [B, H, n, d] and k [B, KV, n, d] (weights [d], or no norm) and their
     rotation, in one pass; returns (q_out, k_out), contiguous unless given (q_out may be q).
     Positions are positions ([n] or [B, n] int32), or start, start + 1, ..."""
-    desc = _rope_desc(q, k, rope, wq, wk, eps, positions, start, False)
-    with _On(q.device, stream) as s:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-        _check("q_out", q_out, q.shape, q.dtype, q.device)
-        _check("k_out", k_out, k.shape, q.dtype, q.device)
-        desc.q_out, desc.k_out = _strides(q_out), _strides(k_out)
+    index, head, strides = _rope_call(q, k, rope, wq, wk, eps, positions, start, False)
+    with _On(index, stream) as s:
+        q_out = q.new_empty(q.shape) if q_out is None else q_out
+        k_out = k.new_empty(k.shape) if k_out is None else k_out
+        desc = _rope_fields(*head, *strides, *_strides("q_out", q_out, q.shape, q.dtype, index)[:3],
+                            *_strides("k_out", k_out, k.shape, q.dtype, index)[:3], *_NO_STRIDES * 2)
         _abi.check(_abi.load().st_qk_norm_rope(_p(q), _p(k), _p(wq), _p(wk), _p(rope.turns), _p(positions), _p(q_out),
                                                _p(k_out), _c.byref(desc), s), "st_qk_norm_rope")
     return q_out, k_out
 
 
-def _rope_bwd_need(desc):
-    return int(_abi.load().st_qk_norm_rope_bwd_workspace_bytes(_c.byref(desc)))
-
-
 def st_qk_norm_rope_bwd_workspace_bytes(q, k, rope: RopeTable) -> int:
-    with _On(q.device, None):
-        return _rope_bwd_need(_rope_desc(q, k, rope, None, None, 0.0, None, 0, False))
+    index, head, strides = _rope_call(q, k, rope, None, None, 0.0, None, 0, False)
+    desc = _rope_fields(*head, *strides, *_NO_STRIDES * 4)
+    with _On(index, None):
+        return int(_abi.load().st_qk_norm_rope_bwd_workspace_bytes(_c.byref(desc)))
 
 
 def st_qk_norm_rope_bwd(q, k, gq, gk, rope: RopeTable, wq=None, wk=None, eps: float = 1e-6, positions=None,
                         start: int = 0, dq=None, dk=None, workspace=None, stream=None):
     """Gradients (dq, dk, dwq, dwk) for the output gradients gq, gk; dwq and dwk are fp32, or None
     without weights.  dq may be gq and dk may be gk."""
-    desc = _rope_desc(q, k, rope, wq, wk, eps, positions, start, False)
+    index, head, strides = _rope_call(q, k, rope, wq, wk, eps, positions, start, False)
+    lib = _abi.load()
     dwq = dwk = None
-    with _On(q.device, stream) as s:
+    with _On(index, stream) as s:
         dq = torch.empty_like(q) if dq is None else dq
         dk = torch.empty_like(k) if dk is None else dk
         for name, t, like in (("gq", gq, q), ("gk", gk, k), ("dq", dq, q), ("dk", dk, k)):
-            _check(name, t, like.shape, q.dtype, q.device)
-        desc.q_out, desc.k_out, desc.dq, desc.dk = _strides(gq), _strides(gk), _strides(dq), _strides(dk)
+            strides += _strides(name, t, like.shape, q.dtype, index)[:3]
+        desc = _rope_fields(*head, *strides)
         if wq is not None:
-            dw = torch.empty((2, q.shape[-1]), dtype=torch.float32, device=q.device)
-            dwq, dwk = dw[0], dw[1]
-            workspace = _workspace(workspace, _rope_bwd_need(desc), q.device)
-        _abi.check(_abi.load().st_qk_norm_rope_bwd(_p(q), _p(k), _p(gq), _p(gk), _p(wq), _p(wk), _p(rope.turns),
-                                                   _p(positions), _p(dq), _p(dk), _p(dwq), _p(dwk), _p(workspace),
-                                                   _nbytes(workspace), _c.byref(desc), s), "st_qk_norm_rope_bwd")
+            dwq, dwk = q.new_empty((2, q.shape[-1]), dtype=torch.float32).unbind()
+            if workspace is None:
+                need = lib.st_qk_norm_rope_bwd_workspace_bytes(_c.byref(desc))
+            workspace = _workspace(workspace, need if workspace is None else 0, q)
+        _abi.check(lib.st_qk_norm_rope_bwd(_p(q), _p(k), _p(gq), _p(gk), _p(wq), _p(wk), _p(rope.turns),
+                                           _p(positions), _p(dq), _p(dk), _p(dwq), _p(dwk), _p(workspace),
+                                           _nbytes(workspace), _c.byref(desc), s), "st_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
@@ -397,21 +415,20 @@ def st_paged_plan(lens, new, block_table, free_pages, free_count, page_size: int
     """Plan a serving step on the device: lens, new [requests], block_table [requests, max_pages]
     (newly taken pages are written in place), free_pages [*] with free_count [1] of them free, all
     int32.  ``tokens`` is the room for new tokens; entries past the last one are -1."""
-    device = lens.device
     if lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("expected lens [requests], block_table [requests, max_pages] and free_pages [*]")
-    R = lens.shape[0]
-    i32 = torch.int32
-    _check_flat("lens", lens, (R,), i32, device)
-    _check_flat("new", new, (R,), i32, device)
-    _check("block_table", block_table, (R, block_table.shape[1]), i32, device)
-    _check_flat("free_pages", free_pages, free_pages.shape, i32, device)
-    _check_flat("free_count", free_count, (1,), i32, device)
-    desc = _abi.st_plan_desc_t(R, tokens, block_table.shape[1], block_table.stride(0), page_size, free_pages.shape[0])
-    with _On(device, stream) as s:
+    R, index, i32 = lens.shape[0], lens.get_device(), torch.int32
+    _check_flat("lens", lens, (R,), i32, index)
+    _check_flat("new", new, (R,), i32, index)
+    max_pages, capacity = block_table.shape[1], free_pages.shape[0]
+    table_stride = _strides("block_table", block_table, (R, max_pages), i32, index)[0]
+    _check_flat("free_pages", free_pages, (capacity,), i32, index)
+    _check_flat("free_count", free_count, (1,), i32, index)
+    desc = _abi.st_plan_desc_t(R, tokens, max_pages, table_stride, page_size, capacity)
+    with _On(index, stream) as s:
         if plan is None:
-            plan = PagedPlan(R, tokens, device)
-        elif plan.requests != R or plan.tokens != tokens or plan.device != device:
+            plan = PagedPlan(R, tokens, lens.device)
+        elif plan.requests != R or plan.tokens != tokens or plan.lens.get_device() != index:
             raise ValueError("plan was made for other sizes or another device")
         _abi.check(_abi.load().st_paged_plan(_p(lens), _p(new), _p(block_table), _p(free_pages), _p(free_count),
                                              _p(plan.lens), _p(plan.free_left), _p(plan.offsets), _p(plan.slots),
@@ -419,13 +436,13 @@ def st_paged_plan(lens, new, block_table, free_pages, free_count, page_size: int
     return plan
 
 
-def _pages(k_pages, v_pages, kv, d, dtype, device):
+def _pages(k_pages, v_pages, kv, d, dtype, index):
+    """Fields of st_pages_t."""
     if k_pages.dim() != 4:
         raise ValueError("pages must be [num_pages, kv_heads, page_size, d]")
-    P, _, ps, _ = k_pages.shape
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _check(name, t, (P, kv, ps, d), dtype, device)
-    return _abi.st_pages_t(P, ps, _strides(k_pages), _strides(v_pages))
+    P, ps = k_pages.shape[0], k_pages.shape[2]
+    shape = (P, kv, ps, d)
+    return (P, ps) + _strides("k_pages", k_pages, shape, dtype, index)[:3] + _strides("v_pages", v_pages, shape, dtype, index)[:3]
 
 
 def st_paged_append(q, k, v, rope: RopeTable, slots, positions, k_pages, v_pages, wq=None, wk=None, eps: float = 1e-6,
@@ -433,18 +450,18 @@ def st_paged_append(q, k, v, rope: RopeTable, slots, positions, k_pages, v_pages
     """New tokens into the cache: q [tokens, H, d] is normed and rotated into q_out, k [tokens, KV, d]
     likewise into its slot of k_pages, v into v_pages ([num_pages, KV, page_size, d] each).  Tokens
     with slot -1 are skipped: their rows of q_out stay as they were (a q_out made here has them 0)."""
-    desc = _rope_desc(q, k, rope, wq, wk, eps, positions, 0, True)
+    index, head, strides = _rope_call(q, k, rope, wq, wk, eps, positions, 0, True)
     n, KV, d = k.shape
-    _check("v", v, k.shape, q.dtype, q.device)
-    _check_flat("slots", slots, (n,), torch.int32, q.device)
+    vs = _abi.st_strides_t(*_by_token(_strides("v", v, k.shape, q.dtype, index)))
+    _check_flat("slots", slots, (n,), torch.int32, index)
     if positions is None or positions.dim() != 1:
         raise ValueError("positions must be [tokens]")
-    pages = _pages(k_pages, v_pages, KV, d, q.dtype, q.device)
-    vs = _token_strides(v)
-    with _On(q.device, stream) as s:
-        q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        _check("q_out", q_out, q.shape, q.dtype, q.device)
-        desc.q_out = _token_strides(q_out)
+    P, ps, *st = _pages(k_pages, v_pages, KV, d, q.dtype, index)
+    pages = _abi.st_pages_t(P, ps, tuple(st[:3]), tuple(st[3:]))
+    with _On(index, stream) as s:
+        q_out = q.new_zeros(q.shape) if q_out is None else q_out
+        qo = _by_token(_strides("q_out", q_out, q.shape, q.dtype, index))
+        desc = _rope_fields(*head, *strides, *qo, *_NO_STRIDES * 3)
         _abi.check(_abi.load().st_paged_append(_p(q), _p(k), _p(v), _p(wq), _p(wk), _p(rope.turns), _p(positions),
                                                _p(slots), _p(q_out), _p(k_pages), _p(v_pages), _c.byref(vs),
                                                _c.byref(pages), _c.byref(desc), s), "st_paged_append")
@@ -453,9 +470,9 @@ def st_paged_append(q, k, v, rope: RopeTable, slots, positions, k_pages, v_pages
 
 def st_paged_decode_workspace_bytes(q, layout: WindowLayout) -> int:
     """Bytes for any decode call of q's shape [requests, H, d] with this layout."""
-    s = _abi.st_strides_t(0, q.shape[2], q.shape[2])
-    desc = _abi.st_paged_desc_t(q.shape[0], q.shape[2], 1, 1, _dtype(q), 0, _abi.st_pages_t(1, 16, s, s))
-    with _On(q.device, None):
+    d = q.shape[2]
+    desc = _paged_fields(q.shape[0], d, 1, 1, _dtype(q), 0, 1, 16, 0, d, d, 0, d, d)
+    with _On(q.get_device(), None):
         return int(layout._lib.st_paged_decode_workspace_bytes(_c.byref(desc), layout.handle))
 
 
@@ -468,22 +485,28 @@ def st_paged_decode(q, k_pages, v_pages, block_table, lens, layout: WindowLayout
     if q.dim() != 3 or block_table.dim() != 2:
         raise ValueError("expected q [requests, heads, d] and block_table [requests, max_pages]")
     R, H, d = q.shape
-    _check_flat("q", q, (R, layout.heads, d), q.dtype, q.device)
-    pages = _pages(k_pages, v_pages, layout.kv_heads, d, q.dtype, q.device)
-    _check("block_table", block_table, (R, block_table.shape[1]), torch.int32, q.device)
-    _check_flat("lens", lens, (R,), torch.int32, q.device)
-    desc = _abi.st_paged_desc_t(R, d, block_table.shape[1], block_table.stride(0), _dtype(q), 0, pages)
-    with _On(q.device, stream) as s:
-        o = torch.empty_like(q) if o is None else o
-        lse = torch.empty((R, H), dtype=torch.float32, device=q.device) if lse is None else lse
-        _check_flat("o", o, q.shape, q.dtype, q.device)
-        _check_flat("lse", lse, (R, H), torch.float32, q.device)
+    index, dtype = q.get_device(), q.dtype
+    _check_flat("q", q, (R, layout.heads, d), dtype, index)
+    pages = _pages(k_pages, v_pages, layout.kv_heads, d, dtype, index)
+    max_pages = block_table.shape[1]
+    table_stride = _strides("block_table", block_table, (R, max_pages), torch.int32, index)[0]
+    _check_flat("lens", lens, (R,), torch.int32, index)
+    desc = _paged_fields(R, d, max_pages, table_stride, _dtype(q), 0, *pages)
+    with _On(index, stream) as s:
+        if o is None:
+            o = torch.empty_like(q)
+        else:
+            _check_flat("o", o, q.shape, dtype, index)
+        if lse is None:
+            lse = q.new_empty((R, H), dtype=torch.float32)
+        else:
+            _check_flat("lse", lse, (R, H), torch.float32, index)
         if workspace is None:
-            need = layout._lib.st_paged_decode_workspace_bytes(_c.byref(desc), layout.handle)
-        workspace = _workspace(workspace, need if workspace is None else 0, q.device)
-        _abi.check(layout._lib.st_paged_decode(_p(q), _p(k_pages), _p(v_pages), _p(block_table), _p(lens), layout.handle,
-                                               _p(o), _p(lse), _p(workspace), _nbytes(workspace), _c.byref(desc), s),
-                   "st_paged_decode")
+            need = layout._lib.st_paged_decode_workspace_bytes(_c.byref(desc), layout._h)
+        workspace = _workspace(workspace, need if workspace is None else 0, q)
+        _abi.check(layout._lib.st_paged_decode(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                                               lens.data_ptr(), layout._h, o.data_ptr(), lse.data_ptr(), _p(workspace),
+                                               _nbytes(workspace), _c.byref(desc), s), "st_paged_decode")
     if check:
         layout.check(stream)
     return o, lse
