@@ -96,15 +96,16 @@ Units plan_units(const st::WindowGeom &g)
 }
 
 struct BwdSizes {
-    size_t delta, entries, parts, maxima;
-    size_t total() const { return delta + entries + parts + maxima; }
+    size_t delta, entries, parts, maxima, counters;
+    size_t total() const { return delta + entries + parts + maxima + counters; }
 };
 
 BwdSizes bwd_sizes(const st::WindowGeom &g, const Units &u, int64_t d)
 {
     const size_t bk = static_cast<size_t>(g.batch) * g.kv;
     return {st::round256(static_cast<size_t>(g.batch) * g.heads * g.nq * sizeof(float)), st::round256(u.entries * sizeof(int2)),
-            bk * u.split * 2 * 128 * d * sizeof(float), st::round256(bk * 2 * sizeof(uint32_t))};
+            bk * u.split * 2 * 128 * d * sizeof(float), st::round256(bk * 2 * sizeof(uint32_t)),
+            256};
 }
 
 }  // namespace
@@ -196,6 +197,7 @@ st_status_t st_window_bwd(const void *q, const void *k, const void *v, const voi
     p.entries = reinterpret_cast<int2 *>(ws + z.delta);
     p.parts = reinterpret_cast<float *>(ws + z.delta + z.entries);
     p.maxima = reinterpret_cast<uint32_t *>(ws + z.delta + z.entries + z.parts);
+    p.counters = reinterpret_cast<int32_t *>(ws + z.delta + z.entries + z.parts + z.maxima);
     p.nentries = u.entries;
     p.nsplit = u.split;
     p.chunk = u.chunk;

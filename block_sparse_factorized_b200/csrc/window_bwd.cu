@@ -23,7 +23,7 @@
 namespace st {
 namespace {
 
-constexpr int THREADS = 384;   // producer, MMA issuer, 2 spare warps, then two softmax warpgroups
+constexpr int THREADS = 384;   // producer, MMA issuer, 2 warps for zeros, then two softmax warpgroups
 constexpr int NSM = 256;       // softmax threads: warpgroup w owns columns 64 w .. of a score tile
 
 template <int DT>
@@ -49,6 +49,73 @@ __device__ __forceinline__ int32_t tile_steps(const WindowGeom &g, int32_t t, in
     return i1 < i0 ? 0 : (i1 - i0 + 1) * g.group;
 }
 
+// Units with steps are taken from a counter as CTAs come to need them, so that a padded batch, whose
+// units differ by what its lengths leave, spreads evenly; which CTA takes a unit changes no sum.  The
+// producer takes them and hands them on through a small ring.  Units
+// without steps never enter the ring (the issuer looks one unit ahead and must not wait for one that
+// is behind several that it does nothing for): two warps that have nothing else to do write their zeros.
+constexpr int NU = 4;
+
+template <typename Unit>
+struct UnitRing {
+    uint64_t full[NU], empty[NU];
+    Unit unit[NU];
+    int32_t steps[NU];  // 0: the end
+
+    __device__ void init()
+    {
+        for (int i = 0; i < NU; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1 + NSM / 32);  // the issuer and each softmax warp
+        }
+    }
+
+    // The producer warp's k-th unit (false: the last was the end, or a wait ran out).  taken: whether
+    // the CTA has had its first number, which is its own.
+    __device__ bool put(const WindowBwdParams &p, int32_t *counter, int32_t k, bool &taken, Unit &U, volatile int32_t *abort, int32_t *err)
+    {
+        bool more;
+        do {
+            int64_t at = blockIdx.x;
+            if (taken) {
+                int32_t n = (threadIdx.x & 31) == 0 ? atomicAdd(counter, 1) : 0;
+                at = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xffffffffu, n, 0);
+            }
+            taken = true;
+            more = get_unit(p, at, U);
+        } while (more && U.steps() == 0);
+        if (k >= NU && !__all_sync(0xffffffffu, mbar_wait(&empty[k % NU], (k / NU - 1) & 1, abort, err))) return false;
+        if ((threadIdx.x & 31) == 0) {
+            unit[k % NU] = U;
+            steps[k % NU] = more ? U.steps() : 0;
+            mbar_arrive(&full[k % NU]);
+        }
+        __syncwarp();
+        return more;
+    }
+
+    // The k-th unit for a softmax warp.
+    __device__ bool take(int32_t k, Unit &U, volatile int32_t *abort, int32_t *err)
+    {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[k % NU], (k / NU) & 1, abort, err))) return false;
+        U = unit[k % NU];
+        const bool more = steps[k % NU] != 0;
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[k % NU]);
+        return more;
+    }
+
+    // The k-th unit's steps for the issuer warp, 0 at the end.  The reduction puts the number where the
+    // compiler knows it to be the same for the warp.
+    __device__ int32_t take_steps(int32_t k, volatile int32_t *abort, int32_t *err)
+    {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[k % NU], (k / NU) & 1, abort, err))) return 0;
+        const int32_t n = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, static_cast<uint32_t>(steps[k % NU])));
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[k % NU]);
+        return n;
+    }
+};
+
 // ---- preparation ------------------------------------------------------------------------------
 // D_i (0 for padding rows), the unit list of dk_dv (block 0: the chunked key tiles first), and for fp16 the largest squared norms
 // of live dO and V rows.  D / 8 lanes a row; memory-bound.
@@ -60,6 +127,7 @@ __global__ void __launch_bounds__(256) window_pre_kernel(const __grid_constant__
     constexpr int L = D / 8, NG = 256 / L;
     const WindowGeom &g = p.g;
     if (blockIdx.x == 0) {  // 256 tiles at a time
+        if (threadIdx.x < 2) p.counters[threadIdx.x] = 0;
         __shared__ int2 sums[8];
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         int32_t split = 0, plain = p.nsplit;  // next entry of a chunked tile, of another
@@ -149,26 +217,20 @@ struct KCfg {
     static constexpr uint32_t OFF_V = TB, OFF_Q = 2 * TB, OFF_DO = OFF_Q + NST * TB, OFF_ROW = OFF_DO + NST * TB;
     static constexpr uint32_t ROW_BYTES = 2 * 128 * 4;        // per stage: -lse (log2 units), -D scaled
     static constexpr uint32_t OFF_BAR = OFF_ROW + NST * ROW_BYTES;
-    static constexpr uint32_t SMEM = OFF_BAR + 256;
-    static constexpr uint32_t COL_S = 0, COL_DP = 128, COL_DV = 256, COL_DK = 256 + D;
+    static constexpr uint32_t SMEM = OFF_BAR + 512;
+    // d = 64 has columns for S of even and odd steps
+    static constexpr int NSB = D == 64 ? 2 : 1;
+    static constexpr uint32_t COL_S = 0, COL_DP = 128 * NSB, COL_DV = COL_DP + 128, COL_DK = COL_DV + D;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-struct KBars {
-    uint64_t k_full, k_empty, v_full, v_empty, qdo_full[4], qdo_empty[4];
-    uint64_t s_full, dp_full, p_ready, ds_ready, acc_full, acc_free, mma_idle;
-    uint32_t tmem_base;
-    int32_t abort;
-};
-static_assert(sizeof(KBars) <= 256, "barrier block");
-
 struct KUnit {
     int32_t b, hk, len, tile, i0, begin, end, entry;
+    __device__ int32_t steps() const { return end - begin; }
 };
 
-__device__ __forceinline__ bool get_unit(const WindowBwdParams &p, int32_t k, KUnit &U)
+__device__ __forceinline__ bool get_unit(const WindowBwdParams &p, int64_t at, KUnit &U)
 {
-    const int64_t at = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     const WindowGeom &g = p.g;
     const int32_t n = g.batch * g.kv;
     if (at >= static_cast<int64_t>(p.nentries) * n) return false;
@@ -189,6 +251,15 @@ __device__ __forceinline__ bool get_unit(const WindowBwdParams &p, int32_t k, KU
     U.end = max(U.begin, min(U.end, last));
     return true;
 }
+
+struct KBars {
+    uint64_t k_full, k_empty, v_full, v_empty, qdo_full[4], qdo_empty[4];
+    uint64_t s_full[2], dp_full, p_ready, ds_ready, acc_full, acc_free, mma_idle;
+    UnitRing<KUnit> units;
+    uint32_t tmem_base;
+    int32_t abort;
+};
+static_assert(sizeof(KBars) <= 512, "barrier block");
 
 template <int DT, int D>
 __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_constant__ WindowBwdParams p)
@@ -212,9 +283,11 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
             mbar_init(&bars->qdo_full[i], 1);
             mbar_init(&bars->qdo_empty[i], 1 + NSM / 32);  // the products, and each softmax warp's row data
         }
-        mbar_init(&bars->s_full, 1);
+        mbar_init(&bars->s_full[0], 1);
+        mbar_init(&bars->s_full[1], 1);
         mbar_init(&bars->dp_full, 1);
         mbar_init(&bars->p_ready, NSM);
+        bars->units.init();
         mbar_init(&bars->ds_ready, NSM);
         mbar_init(&bars->acc_full, 1);
         mbar_init(&bars->acc_free, NSM);
@@ -246,8 +319,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
             bool ok = true;
             auto wait = [&](uint64_t *bar, int32_t n) { return __all_sync(0xffffffffu, mbar_wait(bar, n & 1, abort, err)); };
             KUnit U;
-            for (int32_t k = 0; ok && get_unit(p, k, U); ++k) {
-                if (U.begin == U.end) continue;
+            bool taken = false;
+            for (int32_t k = 0; ok && bars->units.put(p, p.counters, k, taken, U, abort, err); ++k) {
                 const float dsc = g.scale * ds_factor<DT>(p, U.b, U.hk) * exp2f(-PBIAS<DT>);
                 for (int32_t s = U.begin; ok && s < U.end; ++s) {
                     const int st = J % NST;
@@ -312,90 +385,105 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && run) {
+        if (run) {
             constexpr uint32_t id_s = idesc16<DT>(128, 128, false, false);  // S^T, dP^T
             constexpr uint32_t id_a = idesc16<DT>(128, D, false, true);     // dV, dK
             const uint32_t sK = smem_u32(smem), sV = smem_u32(smem + C::OFF_V);
             auto sQ = [&](int32_t t) { return smem_u32(smem + C::OFF_Q + (t % NST) * TB); };
             auto sDO = [&](int32_t t) { return smem_u32(smem + C::OFF_DO + (t % NST) * TB); };
+            auto commit = [&](uint64_t *bar) {
+                if (elect_one()) mma_commit(bar);
+                __syncwarp();
+            };
+            auto wait = [&](uint64_t *bar, int32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err)); };
             auto issue_nn = [&](uint32_t col, uint32_t a, uint32_t b, uint64_t *bar) {
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_bf16_ss(tbase + col, Tile<D>::kmajor(a, k), Tile<D>::kmajor(b, k), id_s, k > 0 ? 1u : 0u);
-                mma_commit(bar);
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_bf16_ss(tbase + col, Tile<D>::kmajor(a, k), Tile<D>::kmajor(b, k), id_s, k > 0 ? 1u : 0u);
+                    mma_commit(bar);
+                }
+                __syncwarp();
             };
             // (P^T or dS^T in TMEM: 8 columns a step of 16 queries, the second 64 queries at + 64) B
             auto issue_acc = [&](uint32_t acc, uint32_t a, uint32_t b, bool first) {
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_bf16_ts(tbase + acc, tbase + a + (k >> 2) * 64 + (k & 3) * 8, Tile<D>::mnmajor(b, k), id_a,
-                                (!first || k > 0) ? 1u : 0u);
-            };
-            KUnit U;
-            int32_t kn = 0, I = 0, J = 0;
-            auto fetch = [&]() {
-                while (get_unit(p, kn, U)) {
-                    ++kn;
-                    if (U.begin < U.end) return true;
+                    for (int k = 0; k < 8; ++k)
+                        mma_bf16_ts(tbase + acc, tbase + a + (k >> 2) * 64 + (k & 3) * 8, Tile<D>::mnmajor(b, k), id_a,
+                                    (!first || k > 0) ? 1u : 0u);
                 }
-                return false;
+                __syncwarp();
             };
-            bool more = fetch();
-            bool ok = !more || (mbar_wait(&bars->k_full, 0, abort, err) && mbar_wait(&bars->qdo_full[0], 0, abort, err));
-            if (more && ok) {
+            int32_t I = 0, J = 0;
+            // S^T of step t, the unit's first or last
+            auto s_of = [&](int32_t t, bool first, bool last) {
+                if ((first && !wait(&bars->k_full, I & 1)) ||
+                    !wait(&bars->qdo_full[t % NST], (t / NST) & 1))
+                    return false;
                 tc_fence_after();
-                issue_nn(C::COL_S, sK, sQ(0), &bars->s_full);
-                if (U.end - U.begin == 1) mma_commit(&bars->k_empty);
-                ok = mbar_wait(&bars->v_full, 0, abort, err);
-                if (ok) {
-                    tc_fence_after();
-                    issue_nn(C::COL_DP, sV, sDO(0), &bars->dp_full);
-                    if (U.end - U.begin == 1) mma_commit(&bars->v_empty);
-                }
-            }
-            // per step: dV += P^T dO | S^T of the next step | dK += dS^T Q | dP^T of the next step
-            int32_t s = U.begin;  // step in the unit
-            while (more && ok) {
-                const int32_t t = J;
-                const bool first = s == U.begin, last = s + 1 == U.end;
-                if (!mbar_wait(&bars->p_ready, t & 1, abort, err)) break;
-                if (first && I > 0 && !mbar_wait(&bars->acc_free, (I - 1) & 1, abort, err)) break;
+                issue_nn(C::COL_S + 128 * (t % C::NSB), sK, sQ(t), &bars->s_full[t % C::NSB]);
+                if (last) commit(&bars->k_empty);
+                return true;
+            };
+            // dP^T of step t, whose dO is there if its S^T has been issued
+            auto dp_of = [&](int32_t t, bool first, bool last) {
+                if (first && !wait(&bars->v_full, I & 1)) return false;
                 tc_fence_after();
-                issue_acc(C::COL_DV, C::COL_S, sDO(t), first);
+                issue_nn(C::COL_DP, sV, sDO(t), &bars->dp_full);
+                if (last) commit(&bars->v_empty);
+                return true;
+            };
+            int32_t n = bars->units.take_steps(0, abort, err), s = 0;  // steps of unit I, the step in it
+            const bool ok = n > 0 && s_of(0, true, n == 1) && dp_of(0, true, n == 1);
+            // per step: dV += P^T dO and S^T of the next step, in this order where they share columns |
+            // dK += dS^T Q | dP^T of the next step
+            while (n > 0 && ok) {
+                const int32_t t = J, i = I;
+                const bool first = s == 0, last = s + 1 == n;
+                ++s;
                 if (last) {
-                    more = fetch();
-                    s = U.begin;
-                    ++I;
-                } else {
-                    ++s;
+                    n = bars->units.take_steps(++I, abort, err);
+                    s = 0;
                 }
-                const bool fin = s + 1 == U.end;  // the next step is its unit's last
-                if (more) {
-                    if ((last && !mbar_wait(&bars->k_full, I & 1, abort, err)) ||
-                        !mbar_wait(&bars->qdo_full[(t + 1) % NST], ((t + 1) / NST) & 1, abort, err))
-                        break;
-                    tc_fence_after();
-                    issue_nn(C::COL_S, sK, sQ(t + 1), &bars->s_full);
-                    if (fin) mma_commit(&bars->k_empty);
-                }
-                if (!mbar_wait(&bars->ds_ready, t & 1, abort, err)) break;
+                const bool more = n > 0, fin = s + 1 == n;  // fin: the next step is its unit's last
+                if (C::NSB == 2 && more && !s_of(t + 1, last, fin)) break;
+                if (!wait(&bars->p_ready, t & 1)) break;
+                if (first && i > 0 && !wait(&bars->acc_free, (i - 1) & 1)) break;
+                tc_fence_after();
+                issue_acc(C::COL_DV, C::COL_S + 128 * (t % C::NSB), sDO(t), first);
+                if (C::NSB == 1 && more && !s_of(t + 1, last, fin)) break;
+                if (!wait(&bars->ds_ready, t & 1)) break;
                 tc_fence_after();
                 issue_acc(C::COL_DK, C::COL_DP, sQ(t), first);
-                mma_commit(&bars->qdo_empty[t % NST]);
-                if (last) mma_commit(&bars->acc_full);
-                if (more) {
-                    if (last && !mbar_wait(&bars->v_full, I & 1, abort, err)) break;
-                    tc_fence_after();
-                    issue_nn(C::COL_DP, sV, sDO(t + 1), &bars->dp_full);
-                    if (fin) mma_commit(&bars->v_empty);
-                }
+                commit(&bars->qdo_empty[t % NST]);
+                if (last) commit(&bars->acc_full);
+                if (more && !dp_of(t + 1, last, fin)) break;
                 ++J;
             }
-            mma_commit(&bars->mma_idle);
+            commit(&bars->mma_idle);
             volatile int32_t never = 0;
             mbar_wait(&bars->mma_idle, 0, &never, err);
         }
-    } else if (warp >= 4) {
+    } else if (warp < 4) {  // zeros of the units without steps
+        const int t = threadIdx.x - 64;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        KUnit U;
+        for (int64_t at = blockIdx.x; get_unit(p, at, U); at += gridDim.x) {
+            if (U.steps() != 0) continue;
+            if (U.entry < p.nsplit) {  // the chunk's partial
+                const int64_t slot = static_cast<int64_t>(U.b * g.kv + U.hk) * p.nsplit + U.entry;
+                uint4 *dst = reinterpret_cast<uint4 *>(p.parts) + slot * (2 * (D / 4) * 128);
+                for (int i = t; i < 2 * (D / 4) * 128; i += 64) dst[i] = zero;
+                continue;
+            }
+            for (int i = t; i < 2 * 128 * (D / 8); i += 64) {
+                const OutTensor &o = i < 128 * (D / 8) ? p.dv : p.dk;
+                const int32_t kpos = U.tile * 128 + i / (D / 8) % 128;
+                if (kpos < g.nk) *reinterpret_cast<uint4 *>(o.p + U.b * o.batch + U.hk * o.head + kpos * o.row + 16 * (i % (D / 8))) = zero;
+            }
+        }
+    } else {
         const int w = (warp - 4) >> 2, q4 = warp & 3, row = q4 * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
         const uint32_t tS = tbase + lane_off + C::COL_S + 64 * w, tDP = tbase + lane_off + C::COL_DP + 64 * w;
@@ -408,7 +496,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
             return ok;
         };
         KUnit U;
-        for (int32_t k = 0; ok && get_unit(p, k, U); ++k) {
+        for (int32_t k = 0; ok; ++k) {
+            if (!bars->units.take(k, U, abort, err)) break;
             const float fac = ds_factor<DT>(p, U.b, U.hk), dsc = g.scale * fac * exp2f(-PBIAS<DT>);
             const uint64_t dsc2 = f32x2(dsc, dsc);
             const int32_t kpos = U.tile * 128 + row;
@@ -421,10 +510,11 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
                 const int32_t lo = kpos < U.len ? kpos - base : 64, up = hi - base;
                 const bool whole = lo <= 0 && up >= 63;
                 uint32_t sv[64];
-                if (!wait_all(&bars->qdo_full[st], J / NST) || !wait_all(&bars->s_full, J)) break;
+                if (!wait_all(&bars->qdo_full[st], J / NST) || !wait_all(&bars->s_full[J % C::NSB], J / C::NSB)) break;
                 const uint32_t rows = smem_u32(smem + C::OFF_ROW + st * C::ROW_BYTES) + 256 * w;
-                tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-                tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+                const uint32_t tSj = tS + 128 * (J % C::NSB);
+                tmem_ld32(tSj, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+                tmem_ld32(tSj + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
                 tmem_wait_ld();
                 const uint64_t keep = whole ? ~0ull : interval_bits64(lo, up);
                 float pr[64];
@@ -447,7 +537,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
                 uint32_t pk[32];
 #pragma unroll
                 for (int c = 0; c < 32; ++c) pk[c] = pack16<DT>(pr[2 * c], pr[2 * c + 1]);
-                tmem_st32(tS, pk);
+                tmem_st32(tSj, pk);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&bars->p_ready);
@@ -481,8 +571,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
                 if (lane == 0) mbar_arrive(&bars->qdo_empty[st]);
             }
             if (!ok) break;
-            const bool any = U.begin < U.end;
-            if (any && !wait_all(&bars->acc_full, I)) break;
+            if (!wait_all(&bars->acc_full, I)) break;
             // dV, then dK: this warpgroup's half of the columns, 32 at a time
 #pragma unroll
             for (int out = 0; out < 2; ++out) {
@@ -491,13 +580,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
                 for (int c = 0; c < D / 64; ++c) {
                     const int col = (D / 2) * w + 32 * c;
                     uint32_t a[32];
-                    if (any) {
-                        tmem_ld32(tbase + lane_off + (out == 0 ? C::COL_DV : C::COL_DK) + col, a);
-                        tmem_wait_ld();
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) a[e] = 0u;
-                    }
+                    tmem_ld32(tbase + lane_off + (out == 0 ? C::COL_DV : C::COL_DK) + col, a);
+                    tmem_wait_ld();
                     if (*abort) continue;
                     if (U.entry < p.nsplit) {  // fp32 partial of this chunk, quads of columns by 128 rows
                         const int64_t slot = static_cast<int64_t>(U.b * g.kv + U.hk) * p.nsplit + U.entry;
@@ -519,11 +603,9 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
                     }
                 }
             }
-            if (any) {
-                ++I;
-                tc_fence_before();
-                mbar_arrive(&bars->acc_free);
-            }
+            ++I;
+            tc_fence_before();
+            mbar_arrive(&bars->acc_free);
         }
     }
     tc_fence_before();
@@ -577,25 +659,17 @@ struct QCfg {
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-struct QBars {
-    uint64_t q_full, q_empty, do_full, do_empty, kv_full[8], kv_empty[8];
-    uint64_t s_full[2], dp_full, dp_free, ds_ready, acc_full, acc_free, mma_idle;
-    uint32_t tmem_base;
-    int32_t abort;
-};
-static_assert(sizeof(QBars) <= 512, "barrier block");
-
 struct QUnit {
-    int32_t b, h, len, row0, steps;
+    int32_t b, h, len, row0;
     KeyRange r;
+    __device__ int32_t steps() const { return r.any ? r.ns + r.kb1 - r.kb0 + 1 : 0; }
     __device__ int32_t tile(int32_t s) const { return s < r.ns ? s : r.kb0 + s - r.ns; }
 };
 
-// Longest (last rows) first, dealt out there and back.
-__device__ __forceinline__ bool get_unit(const WindowBwdParams &p, int32_t k, QUnit &U)
+// Longest (last rows) first.
+__device__ __forceinline__ bool get_unit(const WindowBwdParams &p, int64_t at, QUnit &U)
 {
     const WindowGeom &g = p.g;
-    const int64_t at = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     const int32_t n = g.batch * g.heads;
     if (at >= static_cast<int64_t>(n) * g.nqt) return false;
     const int32_t u = static_cast<int32_t>(at), qi = u / n, bh = u - qi * n;
@@ -604,9 +678,17 @@ __device__ __forceinline__ bool get_unit(const WindowBwdParams &p, int32_t k, QU
     U.len = window_len(g, U.b);
     U.row0 = (g.nqt - 1 - qi) * 128;
     U.r = key_range(g, U.row0, U.len);
-    U.steps = U.r.any ? U.r.ns + U.r.kb1 - U.r.kb0 + 1 : 0;
     return true;
 }
+
+struct QBars {
+    uint64_t q_full, q_empty, do_full, do_empty, kv_full[8], kv_empty[8];
+    uint64_t s_full[2], dp_full, dp_free, ds_ready, acc_full, acc_free, mma_idle;
+    UnitRing<QUnit> units;
+    uint32_t tmem_base;
+    int32_t abort;
+};
+static_assert(sizeof(QBars) <= 512, "barrier block");
 
 template <int DT, int D>
 __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_constant__ WindowBwdParams p)
@@ -633,6 +715,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
         mbar_init(&bars->s_full[0], 1);
         mbar_init(&bars->s_full[1], 1);
         mbar_init(&bars->dp_full, 1);
+        bars->units.init();
         mbar_init(&bars->dp_free, NSM);
         mbar_init(&bars->ds_ready, NSM);
         mbar_init(&bars->acc_full, 1);
@@ -666,10 +749,10 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
             bool ok = true;
             auto wait = [&](uint64_t *bar, int32_t n) { return __all_sync(0xffffffffu, mbar_wait(bar, n & 1, abort, err)); };
             QUnit U;
-            for (int32_t k = 0; ok && get_unit(p, k, U); ++k) {
-                if (U.steps == 0) continue;
+            bool taken = false;
+            for (int32_t k = 0; ok && bars->units.put(p, p.counters + 1, k, taken, U, abort, err); ++k) {
                 const int32_t hk = U.h / g.group;
-                for (int32_t s = 0; ok && s < U.steps; ++s) {
+                for (int32_t s = 0; ok && s < U.steps(); ++s) {
                     const int32_t row = U.tile(s) * 128;
                     for (int v = 0; ok && v < 2; ++v, ++c) {
                         if (s == 0) {  // Q with the first K, dO with the first V
@@ -705,85 +788,92 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && run) {
+        if (run) {
             constexpr uint32_t id_s = idesc16<DT>(128, 128, false, false), id_q = idesc16<DT>(128, D, false, true);
             const uint32_t sQ = smem_u32(smem), sDO = smem_u32(smem + C::OFF_DO);
             auto slot = [&](int32_t c) { return smem_u32(smem + C::OFF_KV + (c % NS) * TB); };
             auto kv_wait = [&](int32_t c) { return mbar_wait(&bars->kv_full[c % NS], (c / NS) & 1, abort, err); };
+            auto commit = [&](uint64_t *bar) {
+                if (elect_one()) mma_commit(bar);
+                __syncwarp();
+            };
+            auto wait = [&](uint64_t *bar, int32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err)); };
             auto issue_nn = [&](uint32_t col, uint32_t a, uint32_t b, uint64_t *bar) {
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_bf16_ss(tbase + col, Tile<D>::kmajor(a, k), Tile<D>::kmajor(b, k), id_s, k > 0 ? 1u : 0u);
-                mma_commit(bar);
-            };
-            // walks the steps of all units: (unit, step) of the step whose S was issued last, and of the
-            // one whose dP was
-            QUnit US{}, UD{};
-            int32_t ks = 0, kd = 0, ss = 0, sd = 0, IS = -1, ID = -1;
-            auto next = [&](QUnit &U, int32_t &k, int32_t &s, int32_t &i) {
-                if (i >= 0 && ++s < U.steps) return true;
-                s = 0;
-                while (get_unit(p, k, U)) {
-                    ++k;
-                    if (U.steps > 0) {
-                        ++i;
-                        return true;
-                    }
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_bf16_ss(tbase + col, Tile<D>::kmajor(a, k), Tile<D>::kmajor(b, k), id_s, k > 0 ? 1u : 0u);
+                    mma_commit(bar);
                 }
-                return false;
+                __syncwarp();
             };
-            auto s_of = [&](int32_t t) {  // S of step t (US, ss)
-                if ((ss == 0 && !mbar_wait(&bars->q_full, IS & 1, abort, err)) || !kv_wait(2 * t)) return false;
+            int32_t n = 0, st = 0, I = -1;  // step st of unit I, which has n, is issued next
+            auto next = [&]() {
+                if (++st < n) return true;
+                n = bars->units.take_steps(++I, abort, err);
+                st = 0;
+                return n > 0;
+            };
+            // S and dP of step t (step st of unit I), dP once that of t - 1 is in registers
+            auto s_dp_of = [&](int32_t t) {
+                if ((st == 0 && !wait(&bars->q_full, I & 1)) || !kv_wait(2 * t)) return false;
                 tc_fence_after();
                 issue_nn(C::COL_S + 128 * (t & 1), sQ, slot(2 * t), &bars->s_full[t & 1]);
-                if (ss + 1 == US.steps) mma_commit(&bars->q_empty);
-                return true;
-            };
-            auto dp_of = [&](int32_t t) {  // dP of step t (UD, sd), once dP of t - 1 is in registers
-                if ((sd == 0 && !mbar_wait(&bars->do_full, ID & 1, abort, err)) || !kv_wait(2 * t + 1) ||
-                    (t > 0 && !mbar_wait(&bars->dp_free, (t - 1) & 1, abort, err)))
+                if (st + 1 == n) commit(&bars->q_empty);
+                if ((st == 0 && !wait(&bars->do_full, I & 1)) || !kv_wait(2 * t + 1) ||
+                    (t > 0 && !wait(&bars->dp_free, (t - 1) & 1)))
                     return false;
                 tc_fence_after();
                 issue_nn(C::COL_DP, sDO, slot(2 * t + 1), &bars->dp_full);
-                mma_commit(&bars->kv_empty[(2 * t + 1) % NS]);
-                if (sd + 1 == UD.steps) mma_commit(&bars->do_empty);
+                commit(&bars->kv_empty[(2 * t + 1) % NS]);
+                if (st + 1 == n) commit(&bars->do_empty);
                 return true;
             };
-            bool have_s = next(US, ks, ss, IS), have_d = next(UD, kd, sd, ID), ok = true;
-            if (have_s) ok = s_of(0);
-            if (ok && have_d) ok = dp_of(0);
-            for (int32_t t = 0; ok && have_d; ++t) {
-                // (UD, sd) is step t
-                const bool first = sd == 0, last = sd + 1 == UD.steps;
-                const int32_t I = ID;
+            bool more = next();
+            const bool ok = more && s_dp_of(0);
+            for (int32_t t = 0; ok && more; ++t) {
+                const bool first = st == 0, last = st + 1 == n;
+                const int32_t i = I;
                 auto dq_of = [&]() {
-                    if (!mbar_wait(&bars->ds_ready, t & 1, abort, err) ||
-                        (first && I > 0 && !mbar_wait(&bars->acc_free, (I - 1) & 1, abort, err)))
+                    if (!wait(&bars->ds_ready, t & 1) ||
+                        (first && i > 0 && !wait(&bars->acc_free, (i - 1) & 1)))
                         return false;
                     tc_fence_after();
                     const uint32_t a = tbase + C::COL_S + 128 * (t & 1), b = slot(2 * t);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_bf16_ts(tbase + C::COL_DQ, a + (k >> 2) * 64 + (k & 3) * 8, Tile<D>::mnmajor(b, k), id_q,
-                                    (!first || k > 0) ? 1u : 0u);
-                    mma_commit(&bars->kv_empty[(2 * t) % NS]);
-                    if (last) mma_commit(&bars->acc_full);
+                        for (int k = 0; k < 8; ++k)
+                            mma_bf16_ts(tbase + C::COL_DQ, a + (k >> 2) * 64 + (k & 3) * 8, Tile<D>::mnmajor(b, k), id_q,
+                                        (!first || k > 0) ? 1u : 0u);
+                    }
+                    __syncwarp();
+                    commit(&bars->kv_empty[(2 * t) % NS]);
+                    if (last) commit(&bars->acc_full);
                     return true;
                 };
                 // the next step's S and dP ahead of dQ, but behind it where they wait for another
                 // unit's Q and dO
-                if (last && !(ok = dq_of())) break;
-                have_s = next(US, ks, ss, IS);
-                if (have_s && !(ok = s_of(t + 1))) break;
-                have_d = next(UD, kd, sd, ID);
-                if (have_d && !(ok = dp_of(t + 1))) break;
-                if (!last && !(ok = dq_of())) break;
+                if (last && !dq_of()) break;
+                more = next();
+                if (more && !s_dp_of(t + 1)) break;
+                if (!last && !dq_of()) break;
             }
-            mma_commit(&bars->mma_idle);
+            commit(&bars->mma_idle);
             volatile int32_t never = 0;
             mbar_wait(&bars->mma_idle, 0, &never, err);
         }
-    } else if (warp >= 4) {
+    } else if (warp < 4) {  // zeros of the units without steps
+        QUnit U;
+        for (int64_t at = blockIdx.x; get_unit(p, at, U); at += gridDim.x) {
+            if (U.steps() != 0) continue;
+            for (int i = threadIdx.x - 64; i < 128 * (D / 8); i += 64) {
+                const int32_t row = U.row0 + i / (D / 8);
+                if (row < g.nq)
+                    *reinterpret_cast<uint4 *>(p.dq.p + U.b * p.dq.batch + U.h * p.dq.head + row * p.dq.row + 16 * (i % (D / 8))) =
+                        make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    } else {
         const int w = (warp - 4) >> 2, q4 = warp & 3, row = q4 * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
         const uint32_t tS = tbase + lane_off + C::COL_S + 64 * w, tDP = tbase + lane_off + C::COL_DP + 64 * w;
@@ -796,7 +886,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
             return ok;
         };
         QUnit U;
-        for (int32_t k = 0; ok && get_unit(p, k, U); ++k) {
+        for (int32_t k = 0; ok; ++k) {
+            if (!bars->units.take(k, U, abort, err)) break;
             const int32_t i = U.row0 + row, pos = g.q_start + i;
             const bool live = i < g.nq && pos < U.len;
             const float fac = ds_factor<DT>(p, U.b, U.h / g.group), dsc = g.scale * fac;
@@ -807,7 +898,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
                 nd = -p.delta[r] * dsc;
             }
             const uint64_t nl2 = f32x2(nlse, nlse), nd2 = f32x2(nd, nd), dsc2 = f32x2(dsc, dsc);
-            for (int32_t s = 0; ok && s < U.steps; ++s, ++J) {
+            for (int32_t s = 0; ok && s < U.steps(); ++s, ++J) {
                 const int32_t base = U.tile(s) * 128 + 64 * w;
                 const bool whole = live && base + 63 <= pos && (g.window == 0 || base > pos - g.window || base + 64 <= g.sinks);
                 const uint64_t keep = whole ? ~0ull : (live ? window_bits64(pos, g.window, g.sinks, base) : 0ull);
@@ -851,17 +942,14 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
                 mbar_arrive(&bars->ds_ready);
             }
             if (!ok) break;
-            const bool any = U.steps > 0;
-            if (any && !wait_all(&bars->acc_full, I)) break;
+            if (!wait_all(&bars->acc_full, I)) break;
             const float f = 1.f / fac;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 const int col = (D / 2) * w + 32 * c;
                 uint32_t a[32];
-                if (any) {
-                    tmem_ld32(tbase + lane_off + C::COL_DQ + col, a);
-                    tmem_wait_ld();
-                }
+                tmem_ld32(tbase + lane_off + C::COL_DQ + col, a);
+                tmem_wait_ld();
                 if (i >= g.nq || *abort) continue;
                 uint4 *dst = reinterpret_cast<uint4 *>(p.dq.p + U.b * p.dq.batch + U.h * p.dq.head + i * p.dq.row + 2 * col);
 #pragma unroll
@@ -872,11 +960,9 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
                     dst[q] = make_uint4(pack16<DT>(x[0], x[1]), pack16<DT>(x[2], x[3]), pack16<DT>(x[4], x[5]), pack16<DT>(x[6], x[7]));
                 }
             }
-            if (any) {
-                ++I;
-                tc_fence_before();
-                mbar_arrive(&bars->acc_free);
-            }
+            ++I;
+            tc_fence_before();
+            mbar_arrive(&bars->acc_free);
         }
     }
     tc_fence_before();
