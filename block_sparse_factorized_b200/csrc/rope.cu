@@ -25,7 +25,10 @@
 namespace st {
 namespace {
 
-constexpr int THREADS = 256;
+// Threads a CTA.  The forward's CTAs end with their items, so small ones, at the same number of warps an
+// SM, leave less of the memory idle at the end (8192 tokens: 55 us with 256, 41 with 128 or 64); the
+// backward's walk, and each leaves a partial row.
+constexpr int FWD_THREADS = 128, THREADS = 256;
 constexpr int U = 4;  // rows a group has in flight
 
 // The lane's part in its group's rows: elements a .. a + 7 and b .. b + 7.
@@ -150,10 +153,12 @@ struct Item {
     int j0, j1;
 };
 
-__device__ __forceinline__ Item item_of(const RopeParams &p, uint32_t i, int nh, int run, int parts)
+__device__ __forceinline__ Item item_of(const RopeParams &p, uint32_t i, int64_t first, int nh, int run, int parts)
 {
     Item r;
-    const uint32_t token = i / static_cast<uint32_t>(parts), part = i - token * parts;
+    uint32_t token = i / static_cast<uint32_t>(parts);
+    const uint32_t part = i - token * parts;
+    token += static_cast<uint32_t>(first);
     r.b = token / static_cast<uint32_t>(p.n);
     r.t = token - static_cast<uint32_t>(r.b) * static_cast<uint32_t>(p.n);
     r.j0 = static_cast<int>(part) * run;
@@ -167,13 +172,15 @@ __device__ __forceinline__ int64_t position(const RopeParams &p, const Item &it)
 }
 
 template <int DT, int L, bool APPEND>
-__global__ void __launch_bounds__(THREADS, DT == ST_FP32 ? 1 : 2) rope_fwd_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(FWD_THREADS, DT == ST_FP32 ? 2 : 4) rope_fwd_kernel(const __grid_constant__ RopeParams p)
 {
-    constexpr int NG = THREADS / L;
+    constexpr int NG = FWD_THREADS / L;
     const Lane<L> w(p);
     const uint32_t i = blockIdx.x * NG + w.grp;
     if (i >= p.items) return;
-    const Item it = item_of(p, i, p.heads + p.kv + (APPEND ? p.kv : 0), p.run, p.parts);
+    const int nh = p.heads + p.kv + (APPEND ? p.kv : 0);
+    const Item it = i < p.tokens0 ? item_of(p, i, 0, nh, nh, 1)
+                                  : item_of(p, i - static_cast<uint32_t>(p.tokens0), p.tokens0, nh, p.run, p.parts);
     int64_t page = 0, at = 0;
     if constexpr (APPEND) {
         const int32_t slot = p.slots[it.t];
@@ -247,7 +254,7 @@ __global__ void __launch_bounds__(THREADS, DT == ST_FP32 ? 1 : 2) rope_bwd_kerne
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.f;
     for (uint32_t i = cta * NG + w.grp; i < items; i += ctas * NG) {
-        const Item it = item_of(p, i, rows, run, parts);
+        const Item it = item_of(p, i, 0, rows, run, parts);
         const int n = it.j1 - it.j0;
         const char *xp = xs.p + it.b * xs.batch + it.t * xs.row + it.j0 * xs.head;
         const char *gp = gs.p + it.b * gs.batch + it.t * gs.row + it.j0 * gs.head;
@@ -323,8 +330,8 @@ template <int DT, int L>
 cudaError_t launch_l(const RopeParams &p, int mode, int64_t grid, cudaStream_t s)
 {
     const unsigned g = static_cast<unsigned>(grid);
-    if (mode == ROPE_FWD) rope_fwd_kernel<DT, L, false><<<g, THREADS, 0, s>>>(p);
-    else if (mode == ROPE_APPEND) rope_fwd_kernel<DT, L, true><<<g, THREADS, 0, s>>>(p);
+    if (mode == ROPE_FWD) rope_fwd_kernel<DT, L, false><<<g, FWD_THREADS, 0, s>>>(p);
+    else if (mode == ROPE_APPEND) rope_fwd_kernel<DT, L, true><<<g, FWD_THREADS, 0, s>>>(p);
     else rope_bwd_kernel<DT, L><<<g, THREADS, 0, s>>>(p);
     return cudaGetLastError();
 }
@@ -338,33 +345,59 @@ cudaError_t launch_t(const RopeParams &p, int mode, int64_t grid, cudaStream_t s
     return launch_l<DT, 16>(p, mode, grid, s);
 }
 
-// Lanes a row, groups a CTA.
+// Lanes a row.
 int lanes_of(int d) { return d <= 32 ? 2 : (d <= 64 ? 4 : (d <= 128 ? 8 : 16)); }
-int groups_of(int d) { return THREADS / lanes_of(d); }
 
-}  // namespace
+// How tokens of `rows` head rows are dealt out: the first `whole` to a group each, of the others `run`
+// rows a group.
+struct RopeSplit {
+    int64_t whole;
+    int32_t run, parts;
+    int64_t items;
+};
 
-RopeSplit rope_split(int64_t tokens, int rows, int d)
+// Runs of the `tokens` tokens, `parts` of them each or fewer; never fewer than U rows.
+RopeSplit split_runs(int64_t whole, int64_t tokens, int64_t parts, int rows)
 {
-    // Rows of a token that one group takes: all of them, unless that leaves fewer groups than the SMs
-    // hold at a time (3 CTAs of 256 threads); never fewer than U, since a group has its angles to compute
-    // and its weights to load first (twice the groups at n = 12288: 65 us in place of 55).
     RopeSplit s;
-    const int64_t groups = 3ll * sm_count() * groups_of(d);
-    int64_t parts = (groups + tokens - 1) / tokens;
     const int64_t most = (rows + U - 1) / U;
     if (parts > most) parts = most;
+    s.whole = whole;
     s.run = static_cast<int>((rows + parts - 1) / parts + U - 1) / U * U;
     s.parts = (rows + s.run - 1) / s.run;
-    s.items = tokens * s.parts;
-    s.ctas = (s.items + groups_of(d) - 1) / groups_of(d);
+    s.items = whole + tokens * s.parts;
     return s;
 }
+
+// A group has its angles to compute and its weights to load first, so tokens stay whole as long as
+// they fill the SMs (4 CTAs each), and what is left over is cut into as many runs as still fit on them
+// at once.  (Append of 8192 tokens, 9472 groups fit: whole 41 us, in two runs 55; 10000 tokens whole 62.)
+RopeSplit fwd_split(int64_t tokens, int rows, int d)
+{
+    const int64_t fit = 4ll * sm_count() * FWD_THREADS / lanes_of(d), rest = tokens % fit;
+    return split_runs(tokens - rest, rest, rest ? fit / rest : 1, rows);
+}
+
+// The backward's groups walk; its runs are as many as the SMs hold groups at a time or some more (768
+// threads).
+RopeSplit bwd_split(int64_t tokens, int rows, int d)
+{
+    const int64_t groups = 768ll * sm_count() / lanes_of(d);
+    return split_runs(0, tokens, (groups + tokens - 1) / tokens, rows);
+}
+
+int64_t ctas_of(const RopeSplit &s, int threads, int d)
+{
+    const int per = threads / lanes_of(d);
+    return (s.items + per - 1) / per;
+}
+
+}  // namespace
 
 RopeCtas rope_bwd_ctas(int64_t tokens, int heads, int kv, int d)
 {
     // Two CTAs an SM that walk, or fewer where the rows run out, dealt out by the rows of each kind.
-    const int64_t q = rope_split(tokens, heads, d).ctas, k = rope_split(tokens, kv, d).ctas;
+    const int64_t q = ctas_of(bwd_split(tokens, heads, d), THREADS, d), k = ctas_of(bwd_split(tokens, kv, d), THREADS, d);
     const int64_t cap = 2ll * sm_count(), share = (cap * kv + (heads + kv) / 2) / (heads + kv);
     const int64_t kc = share < 1 ? 1 : (share > cap - 1 ? cap - 1 : share);
     return {q < cap - kc ? q : cap - kc, k < kc ? k : kc};
@@ -374,13 +407,15 @@ cudaError_t launch_rope(RopeParams &p, int dtype, int mode, float *dwq, float *d
 {
     const int64_t tokens = p.batch * p.n;
     const bool bwd = mode == ROPE_BWD;
-    const RopeSplit r = rope_split(tokens, p.heads + (bwd ? 0 : p.kv + (mode == ROPE_APPEND ? p.kv : 0)), p.d);
+    const RopeSplit r = bwd ? bwd_split(tokens, p.heads, p.d)
+                            : fwd_split(tokens, p.heads + p.kv + (mode == ROPE_APPEND ? p.kv : 0), p.d);
+    p.tokens0 = r.whole;
     p.run = r.run;
     p.parts = r.parts;
     p.items = r.items;
-    int64_t ctas = r.ctas;
+    int64_t ctas = ctas_of(r, FWD_THREADS, p.d);
     if (bwd) {
-        const RopeSplit k = rope_split(tokens, p.kv, p.d);
+        const RopeSplit k = bwd_split(tokens, p.kv, p.d);
         p.run_k = k.run;
         p.parts_k = k.parts;
         p.items_k = k.items;

@@ -23,6 +23,7 @@ struct RopeParams {
     int64_t n, start, pos_batch, page_size, nslots;
     int64_t batch, items;      // items: (token, run of its rows)
     int32_t heads, kv, d, rot, interleaved, w_f32;
+    int64_t tokens0;           // forward: tokens that one group takes whole, before those cut into runs
     int32_t run, parts;        // rows of a run, runs of a token
     int64_t items_k;           // backward: of the keys (the others: of the queries)
     int32_t run_k, parts_k, q_ctas;
@@ -30,12 +31,6 @@ struct RopeParams {
     float *partial;            // backward: [CTAs, d] partial weight gradients
 };
 
-// How `tokens` tokens of `rows` head rows are dealt out.
-struct RopeSplit {
-    int32_t run, parts;
-    int64_t items, ctas;
-};
-RopeSplit rope_split(int64_t tokens, int rows, int d);
 // CTAs of a backward for the queries and for the keys.
 struct RopeCtas {
     int64_t q, k;
