@@ -22,6 +22,8 @@
 //     together), the second in the rows 8 .. 15 that would be empty; rounding it to 8 bits would cost
 //     as much accuracy as the output's own rounding.  With more heads it is rounded to 8 bits (a second
 //     product would cost 13% of the kernel's time), and fp16's 11 bits are kept as they are.
+// Measured, bf16, d = 128, 32 heads on 8 (of 6549 GB/s for a copy): one request of 131072 keys (537 MB)
+// 100 us, 5.4 TB/s; 200 requests of 1 .. 12288 keys behind a window of 4096 (2.8 GB) 475 us, 6.0 TB/s.
 #include "elem.cuh"
 #include "kernels.h"
 #include "lm.h"

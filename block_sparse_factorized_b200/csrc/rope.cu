@@ -17,6 +17,10 @@
 // product in 64-bit integers: exact to 2^-25 turns wherever p stands, and a few integer instructions (in
 // fp64 the conversions alone took a fifth of the kernel's time); a table of cosines would have to be
 // read for every position instead.
+//
+// Measured, bf16, d = 128 (of 6549 GB/s for a copy): forward of 24576 tokens of 16 + 4 heads 51 us,
+// 4.9 TB/s; append of 8192 tokens of 32 + 8 + 8 heads 41 us, 4.8 TB/s; backward of 16390 tokens of 16 + 4
+// heads 70 us, 3.6 TB/s, where the instructions of a row (two reductions and 32 products) still count.
 #include "elem.cuh"
 #include "kernels.h"
 #include "lm.h"
@@ -26,8 +30,8 @@ namespace st {
 namespace {
 
 // Threads a CTA.  The forward's CTAs end with their items, so small ones, at the same number of warps an
-// SM, leave less of the memory idle at the end (8192 tokens: 55 us with 256, 41 with 128 or 64); the
-// backward's walk, and each leaves a partial row.
+// SM, leave less of the memory idle at the end (24576 tokens of 20 rows: 53 us with 256, 51 with 128 or 64);
+// the backward's walk, and each leaves a partial row.
 constexpr int FWD_THREADS = 128, THREADS = 256;
 constexpr int U = 4;  // rows a group has in flight
 

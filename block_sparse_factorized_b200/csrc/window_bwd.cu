@@ -13,6 +13,19 @@
 // A key tile that very many query tiles read (a sink; early keys without a window) is cut into
 // chunks whose fp32 partial sums a third launch adds in order.
 //
+// One CTA an SM, persistent: a producer warp (TMA), a warp that issues the products, two softmax
+// warpgroups with 64 columns each.  The issuing warp walks its steps as a whole and an elected lane issues:
+// in a loop of one lane whose branches depend on loaded values the products' operands stay out of the
+// uniform registers, and the issue itself bounds the kernel (dk_dv 489 us, walking and electing 447).
+//
+// Measured, bf16, n = 12288, 2 x 16 heads on 4, window 1024, 16 sinks (10 d operations a pair, of 1616
+// TFLOP/s for a library product):
+//   d 128   869 us, 577 TFLOP/s: preparation 42, dk_dv 447, join 6, dq 374
+//   d 64    670 us, 374 TFLOP/s: preparation 22, dk_dv 345, join 5, dq 288
+// and 1 x 16 heads over the whole past at d 128: 1875 us, 825 TFLOP/s.  Bound by the chains of a step: at
+// d = 128 a step of dk_dv takes 3400 cycles (2048 of products, which shared memory feeds at its limit), one
+// of dq 2850 (1536); at d = 64 the softmax warps take longer than the products.
+//
 // fp16 has a narrow range: P is kept 2^14 larger, and dS scaled by a power of two per (batch, key
 // head) from the bound |dS| <= 2 max|dO_i| max|v_j| / sqrt d, so that neither overflows nor fades; the
 // results are scaled back in fp32.
@@ -304,6 +317,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = bars->tmem_base;
+    asm volatile("griddepcontrol.launch_dependents;");  // dq needs nothing of this kernel
     const bool run = (*abort == 0);
 
     // I counts units with steps, J steps over all of them.
@@ -971,6 +985,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
         tc_fence_after();
         tmem_dealloc(tbase, 512);
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what follows in the stream follows dk_dv too
 }
 
 template <int DT, int D>
@@ -990,11 +1005,20 @@ cudaError_t launch(const WindowBwdParams &p, cudaStream_t s)
     const int64_t ku = static_cast<int64_t>(p.nentries) * g.batch * g.kv, qu = static_cast<int64_t>(g.batch) * g.heads * g.nqt;
     window_dkdv_kernel<DT, D><<<static_cast<unsigned>(ku < cap ? ku : cap), THREADS, KCfg<D>::SMEM, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (p.nsplit > 0) {
-        window_join_kernel<DT, D><<<static_cast<unsigned>(p.nsplit) * g.batch * g.kv * (D / 4), 128, 0, s>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    window_dq_kernel<DT, D><<<static_cast<unsigned>(qu < cap ? qu : cap), THREADS, QCfg<D>::SMEM, s>>>(p);
+    // dq runs on the SMs that dk_dv leaves or does not need: it starts once every CTA of dk_dv has, and
+    // ends after it.  (All of dk_dv's CTAs fit at once, one an SM, so none waits for an SM that dq holds.)
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(qu < cap ? qu : cap));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = QCfg<D>::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &a;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, window_dq_kernel<DT, D>, p)) != cudaSuccess || p.nsplit == 0) return e;
+    window_join_kernel<DT, D><<<static_cast<unsigned>(p.nsplit) * g.batch * g.kv * (D / 4), 128, 0, s>>>(p);
     return cudaGetLastError();
 }
 

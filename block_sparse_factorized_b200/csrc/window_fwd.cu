@@ -19,8 +19,18 @@
 // d = 64 has TMEM columns for P of its own, so S of the next tile runs during the softmax; at d = 128
 // (S 2 x 128, O 2 x 128) P overwrites S, and the other sub's softmax covers the products.  Units are
 // dealt out in turns (there and back), longest first; no counter, so no memory to clear and the same
-// order every time.  Per 128 x 128 tile the tensor core needs 1024 cycles at d = 128 and the
-// exponentials 1024 cycles of the special-function units.
+// order every time.  Per 128 x 128 tile the tensor core needs 1024 cycles at d = 128 (512 at d = 64) and
+// the exponentials 1024 cycles of the special-function units.
+//
+// Measured, bf16, n = 12288 (of 1616 TFLOP/s for a library product):
+//   d 128, 2 x 16 heads on 4, window 1024, 16 sinks   288 us    695 TFLOP/s
+//   d 128, 1 x 16 heads on 4, the whole past          592 us   1045 TFLOP/s
+//   d 64,  2 x 16 heads on 4, window 1024, 16 sinks   250 us    400 TFLOP/s
+// Bound at d = 64 by the softmax warps: 4400 cycles a pair of tiles, 2050 of them exponentials, the rest
+// latencies of two warps a scheduler (TMEM loads and stores, barriers); starting one sub later changes
+// nothing.  At d = 128 by the chain softmax -> P V -> S of a sub, 4900 cycles a step, 1800 of them waiting
+// for the products, which the other sub's share the tensor core with.  S of a step's first 64 keys ahead of
+// P V, into the columns that P leaves, does not shorten it (307 us): the subs' turns mix again.
 #include <type_traits>
 
 #include "kernels.h"
@@ -273,7 +283,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
             }
         }
     } else if (warp < 3) {
-        if (lane == 0 && run) {
+        if (lane == 0 && run) {  // (the warp walking and one lane elected to issue: 3% slower here)
             const int x = warp - 1;
             constexpr uint32_t idS = idesc16<DT>(128, 128, false, false), idO = idesc16<DT>(128, D, false, true);
             const uint32_t tS = tbase + 128 * x, tO = tbase + C::COL_O + D * x, tP = C::OWN_P ? tbase + C::COL_P + 64 * x : tS;
