@@ -47,7 +47,8 @@ template <int DT>
 __device__ __forceinline__ float ds_factor(const WindowBwdParams &p, int32_t b, int32_t hk)
 {
     if constexpr (DT == ST_BF16) return 1.f;
-    const float a = __uint_as_float(p.maxima[2 * (b * p.g.kv + hk)]), v = __uint_as_float(p.maxima[2 * (b * p.g.kv + hk) + 1]);
+    const uint32_t *most = p.maxima + 2 * (b * p.g.kv + hk);
+    const float a = __uint_as_float(__ldcg(most)), v = __uint_as_float(__ldcg(most + 1));
     const float bound = 2.f * p.g.scale * sqrtf(a) * sqrtf(v);
     if (!(bound > 0.f) || !isfinite(bound)) return 1.f;
     const int e = ilogbf(32768.f / bound);
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(256) window_pre_kernel(const __grid_constant__
 {
     constexpr int L = D / 8, NG = 256 / L;
     const WindowGeom &g = p.g;
+    asm volatile("griddepcontrol.launch_dependents;");
     if (blockIdx.x == 0) {  // 256 tiles at a time
         if (threadIdx.x < 2) p.counters[threadIdx.x] = 0;
         __shared__ int2 sums[8];
@@ -317,7 +319,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = bars->tmem_base;
-    asm volatile("griddepcontrol.launch_dependents;");  // dq needs nothing of this kernel
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the preparation's results
+    asm volatile("griddepcontrol.launch_dependents;");   // dq needs nothing of this kernel
     const bool run = (*abort == 0);
 
     // I counts units with steps, J steps over all of them.
@@ -909,7 +912,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
             if (live) {
                 const int64_t r = (static_cast<int64_t>(U.b) * g.heads + U.h) * g.nq + i;
                 nlse = -p.lse[r] * LOG2E;
-                nd = -p.delta[r] * dsc;
+                nd = -__ldcg(p.delta + r) * dsc;  // (past L1: dq does not wait for the preparation itself)
             }
             const uint64_t nl2 = f32x2(nlse, nlse), nd2 = f32x2(nd, nd), dsc2 = f32x2(dsc, dsc);
             for (int32_t s = 0; ok && s < U.steps(); ++s, ++J) {
@@ -1003,20 +1006,22 @@ cudaError_t launch(const WindowBwdParams &p, cudaStream_t s)
     window_pre_kernel<DT, D><<<static_cast<unsigned>(pre), 256, 0, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t ku = static_cast<int64_t>(p.nentries) * g.batch * g.kv, qu = static_cast<int64_t>(g.batch) * g.heads * g.nqt;
-    window_dkdv_kernel<DT, D><<<static_cast<unsigned>(ku < cap ? ku : cap), THREADS, KCfg<D>::SMEM, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // dq runs on the SMs that dk_dv leaves or does not need: it starts once every CTA of dk_dv has, and
-    // ends after it.  (All of dk_dv's CTAs fit at once, one an SM, so none waits for an SM that dq holds.)
+    // dk_dv is set up while the preparation ends; dq runs on the SMs that dk_dv leaves or does not need: it
+    // starts once every CTA of dk_dv has (and the preparation has ended), and ends after it.  (All of
+    // dk_dv's CTAs fit at once, one an SM, so none waits for an SM that dq holds.)
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(qu < cap ? qu : cap));
+    cfg.gridDim = dim3(static_cast<unsigned>(ku < cap ? ku : cap));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = QCfg<D>::SMEM;
+    cfg.dynamicSmemBytes = KCfg<D>::SMEM;
     cfg.stream = s;
-    cudaLaunchAttribute a{};
-    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    a.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &a;
+    cfg.attrs = &early;
     cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, window_dkdv_kernel<DT, D>, p)) != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(qu < cap ? qu : cap));
+    cfg.dynamicSmemBytes = QCfg<D>::SMEM;
     if ((e = cudaLaunchKernelEx(&cfg, window_dq_kernel<DT, D>, p)) != cudaSuccess || p.nsplit == 0) return e;
     window_join_kernel<DT, D><<<static_cast<unsigned>(p.nsplit) * g.batch * g.kv * (D / 4), 128, 0, s>>>(p);
     return cudaGetLastError();
