@@ -75,7 +75,8 @@ struct Units {
 Units plan_units(const st::WindowGeom &g)
 {
     // A chunk's partial sums cost about five steps' time to write and add (128 KB at d = 128), so
-    // chunks have at least 32; beyond that enough of them for four rounds of the SMs.
+    // chunks have at least 32, or where the SMs would have less than 16 each, down to 8; beyond that
+    // enough of them for four rounds of the SMs.
     int64_t total = 0;
     for (int32_t t = 0; t < g.nkt; ++t) {
         int32_t i0, i1;
@@ -83,8 +84,8 @@ Units plan_units(const st::WindowGeom &g)
         if (i1 >= i0) total += static_cast<int64_t>(i1 - i0 + 1) * g.group;
     }
     total *= static_cast<int64_t>(g.batch) * g.kv;
-    const int64_t even = total / (4ll * st::sm_count());
-    Units u{static_cast<int32_t>(even < 32 ? 32 : (even > MAX_POS ? MAX_POS : even)), 0, 0};
+    const int64_t each = total / st::sm_count(), least = each >= 16 ? 32 : (each <= 4 ? 8 : 2 * each), rounds = each / 4;
+    Units u{static_cast<int32_t>(rounds < least ? least : (rounds > MAX_POS ? MAX_POS : rounds)), 0, 0};
     for (int32_t t = 0; t < g.nkt; ++t) {
         int32_t i0, i1;
         st::query_range(g, t, i0, i1);
