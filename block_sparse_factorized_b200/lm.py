@@ -86,7 +86,7 @@ def _refuse(name, t, shape, dtype, index):
 
 def _check_flat(name, t, shape, dtype, index):
     _strides(name, t, shape, dtype, index)
-    if not t.is_contiguous():
+    if len(shape) > 1 and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
@@ -109,6 +109,8 @@ class _Packer:
 _window_fields = _Packer(_abi.st_window_desc_t, "5q2i24q")
 _rope_fields = _Packer(_abi.st_rope_desc_t, "7q4i2f18q")
 _paged_fields = _Packer(_abi.st_paged_desc_t, "4q2i8q")
+_pages_fields = _Packer(_abi.st_pages_t, "8q")
+_strides_fields = _Packer(_abi.st_strides_t, "3q")
 _NO_STRIDES = (0, 0, 0)
 
 
@@ -331,8 +333,8 @@ def st_qk_norm_rope(q, k, rope: RopeTable, wq=None, wk=None, eps: float = 1e-6, 
     Positions are positions ([n] or [B, n] int32), or start, start + 1, ..."""
     index, head, strides = _rope_call(q, k, rope, wq, wk, eps, positions, start, False)
     with _On(index, stream) as s:
-        q_out = q.new_empty(q.shape) if q_out is None else q_out
-        k_out = k.new_empty(k.shape) if k_out is None else k_out
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format) if k_out is None else k_out
         desc = _rope_fields(*head, *strides, *_strides("q_out", q_out, q.shape, q.dtype, index)[:3],
                             *_strides("k_out", k_out, k.shape, q.dtype, index)[:3], *_NO_STRIDES * 2)
         _abi.check(_abi.load().st_qk_norm_rope(_p(q), _p(k), _p(wq), _p(wk), _p(rope.turns), _p(positions), _p(q_out),
@@ -452,14 +454,13 @@ def st_paged_append(q, k, v, rope: RopeTable, slots, positions, k_pages, v_pages
     with slot -1 are skipped: their rows of q_out stay as they were (a q_out made here has them 0)."""
     index, head, strides = _rope_call(q, k, rope, wq, wk, eps, positions, 0, True)
     n, KV, d = k.shape
-    vs = _abi.st_strides_t(*_by_token(_strides("v", v, k.shape, q.dtype, index)))
+    vs = _strides_fields(*_by_token(_strides("v", v, k.shape, q.dtype, index)))
     _check_flat("slots", slots, (n,), torch.int32, index)
     if positions is None or positions.dim() != 1:
         raise ValueError("positions must be [tokens]")
-    P, ps, *st = _pages(k_pages, v_pages, KV, d, q.dtype, index)
-    pages = _abi.st_pages_t(P, ps, tuple(st[:3]), tuple(st[3:]))
+    pages = _pages_fields(*_pages(k_pages, v_pages, KV, d, q.dtype, index))
     with _On(index, stream) as s:
-        q_out = q.new_zeros(q.shape) if q_out is None else q_out
+        q_out = torch.zeros_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
         qo = _by_token(_strides("q_out", q_out, q.shape, q.dtype, index))
         desc = _rope_fields(*head, *strides, *qo, *_NO_STRIDES * 3)
         _abi.check(_abi.load().st_paged_append(_p(q), _p(k), _p(v), _p(wq), _p(wk), _p(rope.turns), _p(positions),
