@@ -354,3 +354,34 @@ def test_no_second_derivative():
     gq, = torch.autograd.grad(o.float().sum(), q, create_graph=True)
     with pytest.raises(RuntimeError):
         gq.float().sum().backward()
+
+
+@pytest.mark.parametrize("H,KV,d,w,s", [(2, 1, 64, 0, 0), (2, 1, 128, 200, 3), (1, 1, 64, 100, 0)])
+def test_many_empty_sequences(H, KV, d, w, s):
+    """A large batch with few live sequences: long runs of units with nothing to do between others.
+    Live sequences equal themselves alone, bit for bit; all else is zeros."""
+    B, n = 256, 1024
+    lens = [0] * B
+    for b, m in ((3, 1024), (40, 1), (41, 1000), (130, 513), (131, 128), (255, 1024)):
+        lens[b] = m
+    q, k, v, do = inputs(B, H, KV, n, n, d, torch.bfloat16, seed=24)
+    lay = bsf.WindowLayout(H, KV, w, s).upload()
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = bsf.st_window_fwd(q, k, v, lay, lens=ln, check=True)
+    grads = bsf.st_window_bwd(q, k, v, o, lse, do, lay, lens=ln, check=True)
+    dead = torch.tensor([m == 0 for m in lens], device="cuda")
+    assert (o[dead] == 0).all() and (lse[dead] == -math.inf).all() and all((g[dead] == 0).all() for g in grads)
+    for b, m in enumerate(lens):
+        if m == 0:
+            continue
+        one = [t[b:b + 1] for t in (q, k, v)]
+        lb = ln[b:b + 1].contiguous()
+        o1, lse1 = bsf.st_window_fwd(*one, lay, lens=lb, check=True)
+        assert torch.equal(o1[0], o[b]) and torch.equal(lse1[0], lse[b]), b
+        assert (o[b, :, m:] == 0).all() and (lse[b, :, m:] == -math.inf).all()
+        g1 = bsf.st_window_bwd(*one, o1, lse1, do[b:b + 1], lay, lens=lb, check=True)
+        for x, y in zip(g1, grads):
+            # key tiles may be cut into other chunks: fp32 sums in another order, one rounding to bf16 each
+            # (2^-8 of the value on either side; the rest is for sums that cancel)
+            assert torch.allclose(x[0].float(), y[b].float(), rtol=2 ** -6, atol=2 ** -6)
+            assert (y[b, :, m:] == 0).all()
