@@ -19,8 +19,7 @@
 //               (staged, whole rows) after the next unit's first exponentials, while its last product runs
 // d = 64 has TMEM columns for P of its own, so S of the next tile runs during the softmax; at d = 128
 // (S 2 x 128, O 2 x 128) P overwrites S, and the other sub's softmax covers the products.  Units are
-// dealt out in turns (there and back), longest first; no counter, so no memory to clear and the same
-// order every time.  Per 128 x 128 tile the tensor core needs 1024 cycles at d = 128 (512 at d = 64) and
+// dealt out in turns (there and back), longest first; no counter, which would need memory of the call's own.  Per 128 x 128 tile the tensor core needs 1024 cycles at d = 128 (512 at d = 64) and
 // the exponentials 1024 cycles of the special-function units.
 //
 // Measured, bf16, n = 12288 (of 1616 TFLOP/s for a library product):
@@ -89,19 +88,16 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 1024, "barrier block");
 
-// Unit k of this CTA (false: no more).  Longest (last rows) first; odd turns run backwards.
-__device__ __forceinline__ bool get_unit(const WindowFwdParams &p, int32_t k, Unit &U)
+// Units of a batch element and row tile (pair of row tiles).
+__device__ __forceinline__ int32_t unit_cols(const WindowFwdParams &p) { return p.pair_rows ? p.g.heads : p.g.heads / 2; }
+
+// The unit of row tile (or pair) rt and heads c of batch element b.
+__device__ __forceinline__ void make_unit(const WindowFwdParams &p, int32_t b, int32_t rt, int32_t h, Unit &U)
 {
-    const int64_t at = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    U.valid = at < p.units;
-    if (!U.valid) return false;
     const WindowGeom &g = p.g;
-    const int32_t u = static_cast<int32_t>(at), cols = p.pair_rows ? g.heads : g.heads / 2;  // units of a batch element and row tile
-    const int32_t n = cols * g.batch, qi = u / n, hb = u - qi * n;
-    U.b = hb / cols;
-    const int32_t h = hb - U.b * cols;
-    U.len = window_len(g, U.b);
-    const int32_t nrow = p.pair_rows ? (g.nqt + 1) / 2 : g.nqt, rt = nrow - 1 - qi;
+    U.valid = 1;
+    U.b = b;
+    U.len = window_len(g, b);
     KeyRange r[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -116,8 +112,43 @@ __device__ __forceinline__ bool get_unit(const WindowFwdParams &p, int32_t k, Un
         U.ns = min(max(r[0].ns, r[1].ns), U.kb0);
         U.steps = U.ns + kb1 - U.kb0 + 1;
     }
-    return true;
 }
+
+// The units with live rows, as one CTA takes them: 32 batch elements at a time, last row tiles (the longest
+// units) first, dealt out there and back over the CTAs.  Padding is left out before they are dealt, so
+// that a batch of different lengths spreads evenly.  A warp walks them together.
+struct LiveUnits {
+    int32_t b0 = -32, tiles = 0;         // batch elements b0 ..; lane: live row tiles (or pairs) of b0 + lane
+    int32_t rt = 0, base = 0, count = 0; // the row tile walked, units before it, its units
+    int32_t k = 0;
+
+    __device__ bool next(const WindowFwdParams &p, Unit &U)
+    {
+        const WindowGeom &g = p.g;
+        const int lane = threadIdx.x & 31;
+        const int32_t cols = unit_cols(p);
+        const int64_t at = static_cast<int64_t>(k) * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        ++k;
+        U.valid = 0;
+        while (at >= static_cast<int64_t>(base) + count) {
+            base += count;
+            if (--rt < 0) {
+                b0 += 32;
+                if (b0 >= g.batch) return false;
+                const int32_t b = b0 + lane, rows = b < g.batch ? min(g.nq, window_len(g, b) - g.q_start) : 0;
+                tiles = rows > 0 ? (rows + 127) / 128 : 0;
+                if (p.pair_rows) tiles = (tiles + 1) / 2;
+                rt = __reduce_max_sync(0xffffffffu, tiles) - 1;
+            }
+            count = __popc(__ballot_sync(0xffffffffu, tiles > rt && rt >= 0)) * cols;
+        }
+        const int32_t x = static_cast<int32_t>(at - base), nth = x / cols;
+        const uint32_t set = __ballot_sync(0xffffffffu, tiles > rt);
+        const uint32_t it = __ballot_sync(0xffffffffu, tiles > rt && __popc(set & ((1u << lane) - 1u)) == nth);
+        make_unit(p, b0 + __ffs(it) - 1, rt, x - nth * cols, U);
+        return true;
+    }
+};
 
 // Flags of a step: sub x reads the tile, it is the sub's first or last tile of the unit; the unit's
 // first or last step; no more steps.
@@ -224,16 +255,15 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
             bool ok = true;
             auto wait = [&](uint64_t *bar, int32_t n) { return __all_sync(0xffffffffu, mbar_wait(bar, n & 1, abort, err)); };
             Unit U;
-            for (int32_t i = 0, k = 0; ok; ++i) {
-                const bool more = get_unit(p, i, U);
-                if (more && U.steps == 0) continue;
+            LiveUnits units;
+            for (int32_t k = 0; ok; ++k) {
+                const bool more = units.next(p, U);
                 if (k >= NU && !(ok = wait(&bars->u_empty[k % NU], k / NU - 1))) break;
                 if (lane == 0) {
                     bars->units[k % NU] = U;
                     mbar_arrive(&bars->u_full[k % NU]);
                 }
                 if (!more) break;
-                ++k;
                 const int qb = uq % NQB;
                 if (uq >= NQB && !(ok = wait(&bars->q_empty[qb], uq / NQB - 1))) break;
                 ++uq;
@@ -406,7 +436,10 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
         // ahead and must not wait for a step that is behind several units that only the softmax warps,
         // which wait for the issuers, could take.
         Unit U;
-        for (int32_t i = 0; get_unit(p, i, U); ++i) {
+        const int32_t cols = unit_cols(p), n = cols * p.g.batch;
+        for (int64_t at = blockIdx.x; at < p.units; at += gridDim.x) {
+            const int32_t u = static_cast<int32_t>(at), rt = u / n, b = (u - rt * n) / cols;
+            make_unit(p, b, rt, u - rt * n - b * cols, U);
             if (U.steps != 0) continue;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
