@@ -531,12 +531,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
                 const uint32_t rows = smem_u32(smem + C::OFF_ROW + st * C::ROW_BYTES) + 256 * w;
                 const uint32_t tSj = tS + 128 * (J % C::NSB);
                 tmem_ld32(tSj, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-                tmem_ld32(tSj + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
                 tmem_wait_ld();
+                tmem_ld32(tSj + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
                 const uint64_t keep = whole ? ~0ull : interval_bits64(lo, up);
                 float pr[64];
 #pragma unroll
                 for (int c = 0; c < 64; c += 4) {
+                    if (c == 32) tmem_wait_ld();
                     const uint4 r = ld_shared_v4(rows + 4 * c);
                     float x0, x1, x2, x3;
                     f32x2_split(fma2(f32x2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), sc2, f32x2(__uint_as_float(r.x), __uint_as_float(r.y))), x0, x1);
@@ -560,10 +561,11 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
                 mbar_arrive(&bars->p_ready);
                 if (!wait_all(&bars->dp_full, J)) break;
                 tmem_ld32(tDP, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-                tmem_ld32(tDP + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
                 tmem_wait_ld();
+                tmem_ld32(tDP + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
 #pragma unroll
                 for (int c = 0; c < 64; c += 4) {
+                    if (c == 32) tmem_wait_ld();
                     const uint4 r = ld_shared_v4(rows + 512 + 4 * c);
                     float x0, x1, x2, x3;
                     f32x2_split(mul2(f32x2(pr[c], pr[c + 1]), fma2(f32x2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), dsc2, f32x2(__uint_as_float(r.x), __uint_as_float(r.y)))), x0, x1);
