@@ -20,9 +20,9 @@
 //
 // Measured, bf16, n = 12288, 2 x 16 heads on 4, window 1024, 16 sinks (10 d operations a pair, of 1616
 // TFLOP/s for a library product):
-//   d 128   869 us, 577 TFLOP/s: preparation 42, dk_dv 447, join 6, dq 374
-//   d 64    670 us, 374 TFLOP/s: preparation 22, dk_dv 345, join 5, dq 288
-// and 1 x 16 heads over the whole past at d 128: 1875 us, 825 TFLOP/s.  Bound by the chains of a step: at
+//   d 128   840 us, 596 TFLOP/s: preparation 43, dk_dv 460, dq 392 (partly beside dk_dv), join 6
+//   d 64    645 us, 389 TFLOP/s: preparation 23, dk_dv 360, dq 308, join 5
+// and 1 x 16 heads over the whole past at d 128: 1805 us, 857 TFLOP/s.  Bound by the chains of a step: at
 // d = 128 a step of dk_dv takes 3400 cycles (2048 of products, which shared memory feeds at its limit), one
 // of dq 2850 (1536); at d = 64 the softmax warps take longer than the products.
 //
