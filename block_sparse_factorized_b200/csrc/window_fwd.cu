@@ -480,7 +480,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
         // time through the warp's staging
         auto epilogue = [&](bool has_o) {
             if (has_o && !wait_all(&bars->o_done[x], nO)) return false;
-            const float inv = e.l > 0.f ? 1.f / e.l : 0.f;
+            const bool none = e.l == 0.f;  // (a NaN, from a score that is one or +inf, goes through)
+            const float inv = none ? 0.f : 1.f / e.l;
             const int32_t r0 = e.row0 + 32 * q4, rows = *abort == 0 ? p.g.nq - r0 : 0;  // rows to write
             char *dst0 = p.o + e.b * p.o_batch + e.head * p.o_head + (r0 + (lane >> 3)) * p.o_row + 16 * (lane & 7);
 #pragma unroll
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
                         for (int i = 0; i < 8; ++i) a[i] = has_o ? __uint_as_float(o[8 * q + i]) * inv : 0.f;
                         uint32_t w[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) w[i] = inv > 0.f ? pack16<DT>(a[2 * i], a[2 * i + 1]) : 0u;
+                        for (int i = 0; i < 4; ++i) w[i] = none ? 0u : pack16<DT>(a[2 * i], a[2 * i + 1]);
                         st_shared_v4(stg + sw128_off(lane, 4 * c + q), w[0], w[1], w[2], w[3]);
                     }
                 }
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
             }
             if (lane < rows)
                 p.lse[(static_cast<int64_t>(e.b) * p.g.heads + e.head) * p.g.nq + e.row0 + row] =
-                    e.l > 0.f ? (e.m - C::BIAS + lg2(e.l)) * LN2 : -INFINITY;
+                    none ? -INFINITY : (e.m - C::BIAS + lg2(e.l)) * LN2;
             pending = false;
             return true;
         };

@@ -355,7 +355,9 @@ typedef struct {
  *         (clamped to 0 .. nk; NULL: nk).  Rows at positions lens[b] and beyond are padding: O = 0
  *         and lse = -inf; keys there are not seen, whatever they hold (NaN included).
  * o and lse must not overlap each other or an input.
- * A NaN or an infinity in a row before lens[b] may reach any row of its batch element and group.
+ * A row that sees a score of NaN or +inf gets NaN in O and lse.  A NaN or an infinity in a row before
+ * lens[b] may reach O of other rows of its batch element and group too (0 times NaN is NaN).  A row whose
+ * scores are all -inf gets O = 0 and lse = -inf.
  * 16-bit products with fp32 accumulation; the probabilities are rounded to the inputs' type for
  * the second product.
  * Errors: ST_ERR_INVALID_ARG (NULL pointer, sizes, q_start < 0, another device current, an output that

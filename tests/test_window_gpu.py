@@ -385,3 +385,39 @@ def test_many_empty_sequences(H, KV, d, w, s):
             # (2^-8 of the value on either side; the rest is for sums that cancel)
             assert torch.allclose(x[0].float(), y[b].float(), rtol=2 ** -6, atol=2 ** -6)
             assert (y[b, :, m:] == 0).all()
+
+
+@pytest.mark.parametrize("pair", [(4, 2), (3, 1)])  # units of two heads, of two row tiles
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_bad_values_in_live_rows_are_seen(d, dt, pair):
+    """A NaN, or a score of +inf, makes the rows that see it NaN in O and lse (a zero row with an lse of
+    -inf is a padding row's); the other batch elements keep their bits."""
+    (H, KV), B, n, w, s, lens = pair, 4, 333, 100, 4, (333, 260, 333, 130)
+    q, k, v, do = inputs(B, H, KV, n, n, d, DT[dt], seed=31)
+    lay, ln = bsf.WindowLayout(H, KV, w, s).upload(), lens_of(lens)
+    o, lse = bsf.st_window_fwd(q, k, v, lay, lens=ln)
+    clean = (o, lse) + bsf.st_window_bwd(q, k, v, o, lse, do, lay, lens=ln)
+    q[0, 1, 50] = math.nan                   # a query, one of its elements
+    q[0, 0, 200, 3], q[0, 2, 332, d - 1] = math.inf, -math.inf
+    k[0, 0, 120, 5] = math.nan               # a key that a hundred rows see
+    k[1, KV - 1, 2, 7] = math.inf            # a sink
+    v[2, 0, 150, 9] = math.nan               # a value: O alone
+    o, lse = bsf.st_window_fwd(q, k, v, lay, lens=ln, check=True)
+    grads = bsf.st_window_bwd(q, k, v, o, lse, do, lay, lens=ln, check=True)
+    for b in range(3):
+        m = lm_ref.see(n, n, w, s, 0, lens[b], "cuda")
+        for h in range(H):
+            sc = q[b, h].to(F64) @ k[b, h * KV // H].to(F64).T
+            bad = (m & (torch.isnan(sc) | (sc == math.inf))).any(-1)
+            assert torch.equal(torch.isnan(lse[b, h]), bad) and torch.isnan(o[b, h][bad]).all(), (b, h)
+            same = ~bad & m.any(-1) & ~(m & torch.isneginf(sc)).any(-1)  # (a score of -inf counts for nothing)
+            assert ((lse[b, h] - clean[1][b, h])[same].abs() <= 1e-4).all()
+            assert torch.isnan(grads[0][b, h][bad]).all()
+            worse = (m & torch.isnan(v[b, h * KV // H, :, 9])[None]).any(-1)
+            assert torch.isnan(o[b, h, :, 9][worse]).all()
+            dead = ~m.any(-1)
+            assert (o[b, h][dead] == 0).all() and torch.isneginf(lse[b, h][dead]).all()
+        assert torch.isnan(lse[b]).any() == (b < 2) and torch.isnan(o[b]).any()
+    for x, y in zip(clean, (o, lse) + grads):
+        assert torch.equal(x[3], y[3])
