@@ -315,9 +315,10 @@ __global__ void __launch_bounds__(THREADS, PD_CTAS_PER_SM) paged_kernel(const __
                 o1 = fmaf(f, red_o[w][h][x + 1], o1);
             }
             if (full) {
-                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                const bool none = sum == 0.f;  // nothing seen; a NaN, from a score that is one or +inf, goes through
+                const float inv = none ? 0.f : 1.f / sum;
                 reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) + (qrow + h) * D)[x / 2] = pack16<DT>(o0 * inv, o1 * inv);
-                if (x == 0) p.lse[qrow + h] = sum > 0.f ? (mx + lg2(sum)) * LN2 : -INFINITY;
+                if (x == 0) p.lse[qrow + h] = none ? -INFINITY : (mx + lg2(sum)) * LN2;
             } else {
                 *reinterpret_cast<float2 *>(part + 2 * HB + h * D + x) = make_float2(o0, o1);
                 if (x == 0) {
@@ -403,9 +404,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(const __grid_c
         o1 += sum_o[i][x + 1];
     }
     const int64_t q = static_cast<int64_t>(r) * p.heads + hk * p.group + hb * HB + h;
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const bool none = sum == 0.f;
+    const float inv = none ? 0.f : 1.f / sum;
     reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) + q * D)[x / 2] = pack16<DT>(o0 * inv, o1 * inv);
-    if (x == 0) p.lse[q] = sum > 0.f ? (m + lg2(sum)) * LN2 : -INFINITY;
+    if (x == 0) p.lse[q] = none ? -INFINITY : (m + lg2(sum)) * LN2;
 }
 
 template <int DT, int D, int HB>

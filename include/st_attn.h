@@ -485,10 +485,10 @@ ST_API st_status_t st_paged_append(const void *q, const void *k, const void *v, 
  * token's included (clamped to 0 .. max_pages * page_size), so the query stands at lens - 1.  A request
  * of length 0 gets O = 0, lse = -inf.  A key whose page is outside 0 .. num_pages - 1 is not seen, and
  * the window's error word records it (ST_ERR_BAD_PAGE from st_window_check).  Cache rows that are
- * not seen are not used, whatever they hold.  d: 64 or 128; dtype: ST_BF16 or ST_FP16; heads / kv_heads
- * <= 64; requests <= 8192; page_size a multiple of 16; max_pages * page_size <= 2^30.  o, lse and the
- * workspace must not overlap each other or an input.  The order of the sums depends on lens and on the device
- * only: the same inputs give the same bits.
+ * not seen are not used, whatever they hold; a score of NaN or +inf gives NaN in O and lse.  d: 64 or 128;
+ * dtype: ST_BF16 or ST_FP16; heads / kv_heads <= 64; requests <= 8192; page_size a multiple of 16;
+ * max_pages * page_size <= 2^30.  o, lse and the workspace must not overlap each other or an input.  The
+ * order of the sums depends on lens and on the device only: the same inputs give the same bits.
  * Errors: ST_ERR_INVALID_ARG, ST_ERR_UNSUPPORTED, ST_ERR_ALIGNMENT, ST_ERR_NOT_UPLOADED,
  * ST_ERR_WORKSPACE, ST_ERR_CUDA. */
 typedef struct {

@@ -368,3 +368,37 @@ def test_decode_refuses_outputs_that_are_inputs():
     lay = bsf.WindowLayout(4, 2, 0, 0).upload()
     with pytest.raises(bsf.StError):
         bsf.st_paged_decode(q, kp, vp, table, ln, lay, o=q)
+
+
+@pytest.mark.parametrize("H,KV", [(4, 2), (24, 2)])  # 8 rows of a product, 16 rows
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_decode_shows_bad_values_it_sees(dt, d, H, KV):
+    """A NaN, or a score of +inf, among the keys a request sees makes its O and lse NaN (an lse of -inf
+    says that nothing was seen), whether its row is one CTA's or joined from parts."""
+    lens, page, w, s = (40, 9000, 17, 9000, 33), 32, 0, 0
+    kp, vp, table, ln = cache(lens, KV, d, page, dt, seed=40)
+    q = torch.randn(len(lens), H, d, generator=torch.Generator(device="cuda").manual_seed(41), device="cuda").to(DT[dt])
+    lay = bsf.WindowLayout(H, KV, w, s).upload()
+    want = bsf.st_paged_decode(q, kp, vp, table, ln, lay)
+
+    def row(r, j):
+        return int(table[r, j // page]), j % page
+    pg, at = row(0, 39)
+    kp[pg, 1, at, 3] = math.nan              # request 0: one key head
+    pg, at = row(1, 8000)
+    kp[pg, 0, at, d - 1] = math.inf          # request 1: +inf for the heads whose query is above 0 there
+    q[3, 2] = math.nan                       # request 3: one head
+    pg, at = row(4, 5)
+    vp[pg, 0, at, 7] = math.nan              # request 4: a value, O alone
+    o, lse = bsf.st_paged_decode(q, kp, vp, table, ln, lay, check=True)
+    for r, n in enumerate(lens):
+        k = lm_ref.paged_rows(kp, table[r], n, page)
+        sc = q[r].to(F64).view(KV, H // KV, d) @ k.transpose(1, 2)
+        bad = (torch.isnan(sc) | (sc == math.inf)).any(-1).view(H)
+        assert torch.equal(torch.isnan(lse[r]), bad) and torch.isnan(o[r][bad]).all(), r
+        assert torch.equal(lse[r][~bad], want[1][r][~bad]) or r == 1  # (request 1: a key of -inf counts for nothing)
+        assert not torch.isneginf(lse[r]).any()
+    assert torch.isnan(lse[0]).any() and torch.isnan(lse[1]).any() and int(torch.isnan(lse[3]).sum()) == 1
+    assert torch.isnan(o[4, :H // KV, 7]).all() and not torch.isnan(lse[4]).any()
+    assert torch.equal(o[2], want[0][2]) and torch.equal(lse[2], want[1][2])
