@@ -811,12 +811,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
             constexpr uint32_t id_s = idesc16<DT>(128, 128, false, false), id_q = idesc16<DT>(128, D, false, true);
             const uint32_t sQ = smem_u32(smem), sDO = smem_u32(smem + C::OFF_DO);
             auto slot = [&](int32_t c) { return smem_u32(smem + C::OFF_KV + (c % NS) * TB); };
-            auto kv_wait = [&](int32_t c) { return mbar_wait(&bars->kv_full[c % NS], (c / NS) & 1, abort, err); };
             auto commit = [&](uint64_t *bar) {
                 if (elect_one()) mma_commit(bar);
                 __syncwarp();
             };
+            // (a wait that runs out for some lanes only ends it for all: the warp walks as a whole)
             auto wait = [&](uint64_t *bar, int32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err)); };
+            auto kv_wait = [&](int32_t c) { return wait(&bars->kv_full[c % NS], (c / NS) & 1); };
             auto issue_nn = [&](uint32_t col, uint32_t a, uint32_t b, uint64_t *bar) {
                 if (elect_one()) {
 #pragma unroll

@@ -2,6 +2,8 @@
 status, and the rotation speeds against their formulas."""
 import ctypes as c
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -297,3 +299,16 @@ def test_append_refuses_outputs_that_are_other_arrays(lib):
                           (at[8], at[1], at[10]), (at[8], at[9], at[2]), (at[6], at[9], at[10])):
         assert lib.st_paged_append(at[0], at[1], at[2], at[3], at[4], at[5], at[6], at[7], q_out, kp, vp, c.byref(vs),
                                    c.byref(g), c.byref(rope_desc(B=1)), None) == INVALID
+
+
+def test_window_backward_waits_steer_whole_warps():
+    """The roles of the backward's kernels are whole warps that vote, elect and synchronise with full
+    masks, so a bounded wait, which may run out for some lanes and not for others, must not steer lanes
+    apart: its result is put to a vote, or ignored."""
+    with open(os.path.join(os.path.dirname(_abi.__file__), "csrc", "window_bwd.cu")) as f:
+        lines = [x.split("//")[0].strip() for x in f]
+    waits = [x for x in lines if "mbar_wait(" in x]
+    assert len(waits) > 10
+    for x in waits:
+        ignored = re.fullmatch(r"((if|for) \(.*\) )?mbar_wait\(.*, &never, err\);", x)
+        assert ignored or x.count("mbar_wait(") == x.count("__all_sync(0xffffffffu, mbar_wait("), x
