@@ -98,7 +98,7 @@ struct WindowBwdParams {
     float *delta;                    // [batch, heads, nq] D_i (workspace)
     float *parts;                    // fp32 dV, dK partials of chunked key tiles (workspace)
     int2 *entries;                   // (key tile, chunk) units, chunked tiles first (workspace)
-    int32_t *counters;               // next unit of dk_dv, of dq (workspace)
+    int32_t *counters;               // next unit of dk_dv, of dq; whether dq may read (workspace)
     uint32_t *maxima;                // fp16: [batch, kv, 2] largest squared norms of dO and V (workspace)
     int32_t nentries, nsplit, chunk; // units a key head, those of chunked tiles, steps a chunk at most
 };

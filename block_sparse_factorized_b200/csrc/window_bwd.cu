@@ -55,6 +55,30 @@ __device__ __forceinline__ float ds_factor(const WindowBwdParams &p, int32_t b, 
     return ldexpf(1.f, e < -100 ? -100 : (e > 100 ? 100 : e));
 }
 
+// dq runs beside dk_dv and so cannot wait for the grids before it by griddepcontrol.wait, which would
+// wait for dk_dv's end.  What the preparation wrote reaches it through a word instead: dk_dv has waited
+// for the preparation, and releases the word; a thread of each of dq's CTAs acquires it, so that all
+// that dk_dv saw by then, that CTA sees.  The preparation clears the word; dq's CTAs start after dk_dv's
+// first have let them, so the wait is short.
+__device__ __forceinline__ void publish(int32_t *word)
+{
+    asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(word) : "memory");
+}
+
+__device__ __forceinline__ bool await_published(const int32_t *word, int32_t *err)
+{
+    const uint64_t t0 = globaltimer();
+    for (;;) {
+        int32_t x;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(word) : "memory");
+        if (x != 0) return true;
+        if (globaltimer() - t0 > WAIT_NS) {
+            atomicOr(err, ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
 // Chunks of key tile t, and the steps (query tile, head) of it.
 __device__ __forceinline__ int32_t tile_steps(const WindowGeom &g, int32_t t, int32_t &i0)
 {
@@ -142,7 +166,7 @@ __global__ void __launch_bounds__(256) window_pre_kernel(const __grid_constant__
     const WindowGeom &g = p.g;
     asm volatile("griddepcontrol.launch_dependents;");
     if (blockIdx.x == 0) {  // 256 tiles at a time
-        if (threadIdx.x < 2) p.counters[threadIdx.x] = 0;
+        if (threadIdx.x < 3) p.counters[threadIdx.x] = 0;
         __shared__ int2 sums[8];
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         int32_t split = 0, plain = p.nsplit;  // next entry of a chunked tile, of another
@@ -320,7 +344,9 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkdv_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tbase = bars->tmem_base;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the preparation's results
-    asm volatile("griddepcontrol.launch_dependents;");   // dq needs nothing of this kernel
+    // ... and handed on to dq, which starts beside this kernel and needs nothing else of it
+    if (blockIdx.x == 0 && threadIdx.x == 0) publish(p.counters + 2);
+    asm volatile("griddepcontrol.launch_dependents;");
     const bool run = (*abort == 0);
 
     // I counts units with steps, J steps over all of them.
@@ -743,6 +769,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
         bars->abort = (smem_u32(smem) & 1023u) ? 1 : 0;
         if (bars->abort) atomicOr(err, 2);
         fence_barrier_init();
+        // D, the maxima and the counters: the barrier below passes them on to the CTA
+        if (!await_published(p.counters + 2, err)) bars->abort = 1;
     }
     if (warp == 1) {
         tmem_alloc(&bars->tmem_base, 512);
@@ -915,7 +943,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
             if (live) {
                 const int64_t r = (static_cast<int64_t>(U.b) * g.heads + U.h) * g.nq + i;
                 nlse = -p.lse[r] * LOG2E;
-                nd = -__ldcg(p.delta + r) * dsc;  // (past L1: dq does not wait for the preparation itself)
+                nd = -__ldcg(p.delta + r) * dsc;
             }
             const uint64_t nl2 = f32x2(nlse, nlse), nd2 = f32x2(nd, nd), dsc2 = f32x2(dsc, dsc);
             for (int32_t s = 0; ok && s < U.steps(); ++s, ++J) {
@@ -1010,8 +1038,8 @@ cudaError_t launch(const WindowBwdParams &p, cudaStream_t s)
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t ku = static_cast<int64_t>(p.nentries) * g.batch * g.kv, qu = static_cast<int64_t>(g.batch) * g.heads * g.nqt;
     // dk_dv is set up while the preparation ends; dq runs on the SMs that dk_dv leaves or does not need: it
-    // starts once every CTA of dk_dv has (and the preparation has ended), and ends after it.  (All of
-    // dk_dv's CTAs fit at once, one an SM, so none waits for an SM that dq holds.)
+    // starts once every CTA of dk_dv has (and the preparation has ended; await_published), and ends after it.
+    // (All of dk_dv's CTAs fit at once, one an SM, so none waits for an SM that dq holds.)
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;

@@ -421,3 +421,34 @@ def test_bad_values_in_live_rows_are_seen(d, dt, pair):
         assert torch.isnan(lse[b]).any() == (b < 2) and torch.isnan(o[b]).any()
     for x, y in zip(clean, (o, lse) + grads):
         assert torch.equal(x[3], y[3])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("n,d", [(60, 64), (700, 128), (2500, 64)])
+def test_backward_over_one_workspace(n, d, dt):
+    """Calls behind one another on one workspace, whatever it held: each sees its own preparation (D, the
+    maxima, the counters), in a graph's replays too."""
+    lay = bsf.WindowLayout(4, 2, 90, 4).upload()
+    calls, want = [], []
+    for i in range(6):
+        q, k, v, do = inputs(2, 4, 2, n, n, d, DT[dt], seed=50 + i)
+        do = do * 4.0 ** i  # (fp16: another factor on dS each time)
+        o, lse = bsf.st_window_fwd(q, k, v, lay)
+        calls.append((q, k, v, o, lse, do))
+        want.append(bsf.st_window_bwd(*calls[-1], lay))
+    ws = torch.empty(bsf.st_window_bwd_workspace_bytes(calls[0][0], calls[0][1], lay), dtype=torch.uint8, device="cuda")
+    for fill in (0, 1, 255):
+        ws.fill_(fill)
+        got = [bsf.st_window_bwd(*x, lay, workspace=ws) for x in calls for _ in range(3)]
+        lay.check()
+        assert all(torch.equal(a, b) for i, g in enumerate(got) for a, b in zip(g, want[i // 3]))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = [bsf.st_window_bwd(*x, lay, workspace=ws) for x in calls]
+    for _ in range(3):
+        for x in out:
+            for t in x:
+                t.fill_(7.0)
+        g.replay()
+        lay.check()
+        assert all(torch.equal(a, b) for x, w in zip(out, want) for a, b in zip(x, w))
