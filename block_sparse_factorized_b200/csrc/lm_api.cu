@@ -247,9 +247,10 @@ st_status_t st_paged_plan(const int32_t *lens, const int32_t *new_tokens, int32_
 {
     const void *ptrs[] = {lens, new_tokens, block_table, free_pages, free_count, lens_out,
                           free_left, offsets, slots, positions, status};
-    for (const void *x : ptrs)
-        if (!x) return ST_ERR_INVALID_ARG;
-    if (!desc || desc->requests < 1 || desc->tokens < 1 || desc->tokens > MAX_POS || desc->max_pages < 1 ||
+    if (!desc) return ST_ERR_INVALID_ARG;
+    for (int i = 0; i < 11; ++i)
+        if (!ptrs[i] && !(i == 3 && desc->free_capacity == 0)) return ST_ERR_INVALID_ARG;  // (an empty list is not read)
+    if (desc->requests < 1 || desc->tokens < 1 || desc->tokens > MAX_POS || desc->max_pages < 1 ||
         desc->max_pages > (1 << 24) || desc->page_size < 1 || desc->page_size > (1 << 20) || desc->free_capacity < 0 ||
         desc->free_capacity > INT32_MAX || (desc->requests > 1 && desc->table_stride < desc->max_pages) ||
         desc->table_stride > (1ll << 38))
@@ -262,7 +263,7 @@ st_status_t st_paged_plan(const int32_t *lens, const int32_t *new_tokens, int32_
     for (int i = 0; i < 11; ++i) {
         if (!aligned_to(ptrs[i], 4)) return ST_ERR_ALIGNMENT;
         for (int j = 0; j < i; ++j) {
-            if (i < 5 && i != 2 && j != 2) continue;  // two inputs
+            if ((i < 5 && i != 2 && j != 2) || words[i] == 0 || words[j] == 0) continue;  // two inputs, or no elements
             const auto a = reinterpret_cast<uintptr_t>(ptrs[i]), b = reinterpret_cast<uintptr_t>(ptrs[j]);
             if (a < b + 4 * words[j] && b < a + 4 * words[i]) return ST_ERR_INVALID_ARG;
         }

@@ -455,8 +455,9 @@ typedef struct {
  *   slots, positions [tokens]: of each token; -1 for tokens of a request not served and for entries
  *              past the last token (and the slot of a token whose block table entry is negative)
  *   status     [requests]: 0 served, 1 not served
- * Inputs and outputs must not overlap (block_table apart).  requests: 1 .. 8192; tokens: 1 .. 2^30;
- * page_size: 1 .. 2^20; max_pages: 1 .. 2^24.  Slots are 32-bit: a slot past 2^31 - 1 is given as -1.
+ * free_pages may be NULL where free_capacity is 0.  Inputs and outputs must not overlap (block_table
+ * apart).  requests: 1 .. 8192; tokens: 1 .. 2^30; page_size: 1 .. 2^20; max_pages: 1 .. 2^24.  Slots are
+ * 32-bit: a slot past 2^31 - 1 is given as -1.
  * Errors: ST_ERR_INVALID_ARG (NULL pointer, sizes, an output that is an input), ST_ERR_UNSUPPORTED
  * (requests > 8192), ST_ERR_CUDA. */
 typedef struct {

@@ -312,3 +312,13 @@ def test_window_backward_waits_steer_whole_warps():
     for x in waits:
         ignored = re.fullmatch(r"((if|for) \(.*\) )?mbar_wait\(.*, &never, err\);", x)
         assert ignored or x.count("mbar_wait(") == x.count("__all_sync(0xffffffffu, mbar_wait("), x
+
+
+def test_plan_takes_an_empty_free_list(lib):
+    """No free pages: NULL with a capacity of 0 (PyTorch's pointer to no elements) gets past the checks of
+    pointers and overlaps, to the last refusal here; with a capacity it is refused."""
+    assert plan_args(lib, F=0, free=None, status=P + 2) == ALIGNMENT
+    assert plan_args(lib, F=1, free=None, status=P + 2) == INVALID
+    assert plan_args(lib, F=0, free=None, alias=("lens_out", "lens", 0)) == INVALID
+    assert plan_args(lib, F=0, free=None, lens=None) == INVALID
+    assert plan_args(lib, F=0, alias=("free", "slots", 1), status=P + 2) == ALIGNMENT  # (no elements overlap nothing)

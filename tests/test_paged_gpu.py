@@ -402,3 +402,11 @@ def test_decode_shows_bad_values_it_sees(dt, d, H, KV):
     assert torch.isnan(lse[0]).any() and torch.isnan(lse[1]).any() and int(torch.isnan(lse[3]).sum()) == 1
     assert torch.isnan(o[4, :H // KV, 7]).all() and not torch.isnan(lse[4]).any()
     assert torch.equal(o[2], want[0][2]) and torch.equal(lse[2], want[1][2])
+
+
+def test_plan_with_no_free_pages():
+    """A full cache and an empty list: requests with room in their last page are served, others are not."""
+    run_plan([17, 16, 0, 47], [1, 1, 0, 1], [[3, 5, -1], [7, -1, -1], [-1, -1, -1], [2, 9, 1]], [], 0, 16, 8)
+    run_plan([17, 16, 0, 47], [1, 1, 0, 1], [[3, 5, -1], [7, -1, -1], [-1, -1, -1], [2, 9, 1]], [], 5, 16, 8)
+    lens, new, table, _ = random_state(1500, 16, 6, 90, 3, 6)
+    run_plan(lens, new, table, [], 0, 16, 5000)
