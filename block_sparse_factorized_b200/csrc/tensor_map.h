@@ -37,10 +37,18 @@ inline bool encode(CUtensorMap *m, const void *base, CUtensorMapDataType dt, cuu
             CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B)
 {
     const cuuint32_t es[4] = {1, 1, 1, 1};
-    return encode_fn()(m, dt, rank, const_cast<void *>(base), dims, strides, box, es,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    auto run = [&]() {
+        return encode_fn()(m, dt, rank, const_cast<void *>(base), dims, strides, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (run()) return true;
+    // The encoder is a driver call: it fails where the calling thread has no context current yet, as
+    // where this is the thread's first CUDA call (a framework's backward thread); the runtime makes the
+    // device's own current.
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && run();
 }
 
 }  // namespace st

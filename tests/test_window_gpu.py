@@ -2,6 +2,7 @@
 lm_ref.py, element by element within the roundings' bounds, and the calls a user may make of it:
 strided views, padded batches with garbage in the padding, graphs, streams, extreme values."""
 import math
+import threading
 
 import pytest
 import torch
@@ -452,3 +453,54 @@ def test_backward_over_one_workspace(n, d, dt):
         g.replay()
         lay.check()
         assert all(torch.equal(a, b) for x, w in zip(out, want) for a, b in zip(x, w))
+
+
+def in_a_thread(f):
+    """f() in a thread that has made no CUDA call: its result, or its exception raised here."""
+    out = []
+
+    def run():
+        try:
+            out.append((f(), None))
+        except BaseException as e:  # noqa: BLE001
+            out.append((None, e))
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    if out[0][1] is not None:
+        raise out[0][1]
+    return out[0][0]
+
+
+def test_first_cuda_call_of_a_thread():
+    """Each call as the first that its thread makes (as PyTorch's backward runs in a thread of its own):
+    no context is current there yet."""
+    q, k, v, do = inputs(1, 4, 4, 256, 256, 64, torch.bfloat16, seed=60)
+    lay, t = bsf.WindowLayout(4, 4, 60, 2).upload(), bsf.RopeTable(64, device="cuda")
+    fixed = bsf.Layout(bsf.ST_FIXED, bsf.ST_PER_HEAD_ALTERNATING, 4, 256, 128, 32).upload()
+    o, lse = bsf.st_window_fwd(q, k, v, lay)
+    fo, flse = bsf.st_attn_fwd(q, k, v, fixed)
+    pages = [x[0].view(4, 16, 16, 64).transpose(0, 1).contiguous() for x in (k, v)]
+    table, i = torch.arange(16, dtype=torch.int32, device="cuda")[None], torch.arange(256, dtype=torch.int32, device="cuda")
+    tok = [x[0].transpose(0, 1) for x in (q, k, v)]
+    calls = {
+        "window_fwd": lambda: bsf.st_window_fwd(q, k, v, lay),
+        "window_bwd": lambda: bsf.st_window_bwd(q, k, v, o, lse, do, lay),
+        "rope": lambda: bsf.st_qk_norm_rope(q, k, t),
+        "rope_bwd": lambda: bsf.st_qk_norm_rope_bwd(q, k, do, do, t)[:2],
+        "plan": lambda: (bsf.st_paged_plan(i[:1], i[3:4], table.clone(), i, i[9:10], 16, 8).slots,),
+        "append": lambda: (bsf.st_paged_append(*tok, t, i, i, *[x.clone() for x in pages]),),
+        "decode": lambda: bsf.st_paged_decode(tok[0][-1:].contiguous(), *pages, table, i[255:], lay),
+        "attn_fwd": lambda: bsf.st_attn_fwd(q, k, v, fixed),
+        "attn_bwd": lambda: bsf.st_attn_bwd(q, k, v, fo, flse, do, fixed),
+        "attn_decode": lambda: bsf.st_attn_decode(q[:, :, 255].contiguous(), k, v, fixed, 255),
+    }
+    for name, f in calls.items():
+        want = f()
+        torch.cuda.synchronize()
+        kept = [x.clone() for x in want]
+        del want  # its memory is there for the thread's call, which need not allocate
+        torch.cuda.synchronize()
+        got = in_a_thread(f)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(kept, got)), name
