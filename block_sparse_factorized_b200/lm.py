@@ -248,7 +248,7 @@ def _as_rows(t):
     es = t.element_size()
     ok = t.data_ptr() % 16 == 0 and t.stride(-1) == 1 and all(
         t.shape[i] == 1 or (t.stride(i) >= t.shape[-1] and t.stride(i) * es % 16 == 0) for i in range(t.dim() - 1))
-    return t if ok else t.contiguous()
+    return t if ok else t.clone(memory_format=torch.contiguous_format)  # (contiguous() keeps a slice off a boundary)
 
 
 class WindowAttention(torch.autograd.Function):

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import lm_ref
-from block_sparse_factorized_b200 import _abi
+from block_sparse_factorized_b200 import _abi, lm
 
 bsf = pytest.importorskip("block_sparse_factorized_b200")
 
@@ -322,3 +322,19 @@ def test_plan_takes_an_empty_free_list(lib):
     assert plan_args(lib, F=0, free=None, alias=("lens_out", "lens", 0)) == INVALID
     assert plan_args(lib, F=0, free=None, lens=None) == INVALID
     assert plan_args(lib, F=0, alias=("free", "slots", 1), status=P + 2) == ALIGNMENT  # (no elements overlap nothing)
+
+
+def test_gradients_are_brought_to_aligned_rows():
+    """What PyTorch may hand a backward: slices that start off a 16-byte boundary though contiguous (the
+    gradient of a concatenation), expanded and transposed ones; all come out as the kernels read them."""
+    x = torch.arange(2 * 3 * 5 * 64 + 8, dtype=torch.float32).bfloat16()
+    odd = x[3:3 + 2 * 3 * 5 * 64].view(2, 3, 5, 64)
+    assert odd.data_ptr() % 16 != 0 and odd.is_contiguous()
+    even = x[:2 * 3 * 5 * 64].view(2, 3, 5, 64)
+    one = x[1:65].view(1, 1, 1, 64)  # strides of dimensions of extent 1 are not read, the address is
+    for t in (odd, even, one, even[:, :, :, :1].expand(2, 3, 5, 64), even[:, :1].expand(2, 3, 5, 64), even.transpose(1, 2),
+              x[:2 * 3 * 5 * 64].view(2, 3, 64, 5).transpose(2, 3), x[:1].expand(2, 3, 5, 64)):
+        y = lm._as_rows(t)
+        assert torch.equal(y, t) and y.data_ptr() % 16 == 0 and y.stride(-1) == 1
+        assert all(n == 1 or (s >= 64 and s % 8 == 0) for n, s in zip(y.shape[:-1], y.stride()))
+    assert lm._as_rows(even) is even and lm._as_rows(even.transpose(1, 2)).data_ptr() == even.data_ptr()

@@ -178,3 +178,35 @@ def test_autograd():
     got = x.grad.view(B, n, H + 2 * KV, d).transpose(1, 2)
     for a, b in ((got[:, :H], dq), (got[:, H:H + KV], dk), (got[:, H + KV:], gv), (wq.grad, dwq.bfloat16()), (wk.grad, dwk.bfloat16())):
         assert torch.equal(a, b)
+
+
+def test_autograd_of_a_concatenation():
+    """Gradients that come as slices of a larger one, off a 16-byte boundary."""
+    B, n, H, KV, d = 1, 33, 4, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q, k, v = (torch.randn(B, h, n, d, generator=g, device="cuda").bfloat16().requires_grad_() for h in (H, KV, KV))
+    t, lay = bsf.RopeTable(d, device="cuda"), bsf.WindowLayout(H, KV, 20, 2).upload()
+    extra = torch.randn(3, generator=g, device="cuda").bfloat16()
+    w = [torch.randn(3 + B * h * n * d, generator=g, device="cuda").bfloat16() for h in (H, H, KV)]
+
+    def grads(head):
+        qr, kr = bsf.QKNormRope.apply(q, k, None, None, t)
+        o = bsf.WindowAttention.apply(qr, kr, v, lay)
+        loss = sum((torch.cat([extra, x.flatten()]) * y).sum() if head else (x.flatten() * y[3:]).sum()
+                   for x, y in zip((o, qr, kr), w))
+        return torch.autograd.grad(loss, (q, k, v))
+    for a, b in zip(grads(True), grads(False)):
+        assert torch.equal(a, b)
+
+
+def test_autograd_of_slices_alone():
+    """The same for each operator by itself: its only gradient is such a slice."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    q, k = (torch.randn(1, h, 5, 64, generator=g, device="cuda").bfloat16().requires_grad_() for h in (2, 1))
+    one = torch.zeros(1, device="cuda").bfloat16()
+    t, lay = bsf.RopeTable(64, device="cuda"), bsf.WindowLayout(2, 1, 0, 0).upload()
+    for f in (lambda: bsf.QKNormRope.apply(q, k, None, None, t)[0], lambda: bsf.WindowAttention.apply(q, k, k, lay)):
+        w = torch.randn(2 * 5 * 64, generator=g, device="cuda").bfloat16()
+        a = torch.autograd.grad(torch.cat([one, f().flatten()]), q, torch.cat([one, w]))[0]
+        b = torch.autograd.grad(f(), q, w.view(1, 2, 5, 64))[0]
+        assert torch.equal(a, b)
