@@ -35,7 +35,6 @@ ST_HD int32_t window_len(const WindowGeom &g, int32_t b)
 struct KeyRange {
     int32_t kb0, kb1, ns;
     bool any;                    // some row of the tile is live
-    ST_HD bool has(int32_t t) const { return any && (t < ns || (t >= kb0 && t <= kb1)); }
 };
 
 // Rows row0 .. row0 + 127 of a sequence of length len.
