@@ -504,3 +504,45 @@ def test_first_cuda_call_of_a_thread():
         got = in_a_thread(f)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(kept, got)), name
+
+
+def test_backward_offsets_past_32_bits():
+    """The backward over tensors of more than 2^31 elements, with a sequence's end inside a tile: the last
+    head's last rows."""
+    B, H, n, d, w, m = 1, 9, 2_000_000, 128, 200, 700
+    end = n - 50
+    q = torch.zeros(B, H, n, d, dtype=torch.bfloat16, device="cuda")
+    k, v, do = (torch.zeros_like(q) for _ in range(3))
+    assert q.numel() > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(18)
+    for t in (q, k, v, do):
+        t[0, -1, -m:] = torch.randn(m, d, generator=g, device="cuda").bfloat16()
+    lay = bsf.WindowLayout(H, H, w, 0).upload()
+    ln = lens_of((end,))
+    o, lse = bsf.st_window_fwd(q, k, v, lay, lens=ln, check=True)
+    got = bsf.st_window_bwd(q, k, v, o, lse, do, lay, lens=ln, check=True)
+    a = [t[:, -1:, -m:] for t in (q, k, v, o, lse, do)]
+    want = lm_ref.window_grads(*a, w, 0, q_start=0, lens=(m - 50,))
+    # every query that sees these keys is among these rows, so dK and dV are whole; dQ where the window is
+    for i, (x, (ref, bound)) in enumerate(zip(got, want)):
+        rows = slice(w if i == 0 else 0, m)
+        err = (x[:, -1:, -m:].to(F64) - ref).abs()[:, :, rows]
+        assert (err <= bound[:, :, rows]).all(), f"{i}: worst {(err / bound[:, :, rows]).max():.3f} of the bound"
+        assert (x[:, -1:, -50:] == 0).all() and (x[:, :-1] == 0).all()
+
+
+@pytest.mark.parametrize("H,KV,d,w,s", [(2, 1, 64, 0, 0), (2, 1, 128, 200, 3), (1, 1, 64, 100, 0)])
+def test_gradients_among_many_empty_sequences(H, KV, d, w, s):
+    """The live sequences of such a batch against the formulas, by the derived bounds."""
+    B, n = 256, 1024
+    lens = [0] * B
+    for b, m in ((3, 1024), (40, 1), (41, 1000), (130, 513), (131, 128), (255, 1024)):
+        lens[b] = m
+    q, k, v, do = inputs(B, H, KV, n, n, d, torch.bfloat16, seed=25)
+    lay = bsf.WindowLayout(H, KV, w, s).upload()
+    ln = lens_of(lens)
+    o, lse = bsf.st_window_fwd(q, k, v, lay, lens=ln, check=True)
+    got = bsf.st_window_bwd(q, k, v, o, lse, do, lay, lens=ln, check=True)
+    for b in [b for b in range(B) if lens[b]]:
+        a = [t[b:b + 1] for t in (q, k, v, o, lse, do)]
+        lm_ref.check_grads([t[b:b + 1] for t in got], lm_ref.window_grads(*a, w, s, lens=(lens[b],)))
