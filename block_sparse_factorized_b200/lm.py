@@ -285,7 +285,7 @@ class RopeTable:
                  original: float = 8192, interleaved: bool = False, device="cuda"):
         if scaling not in _SCALINGS:
             raise ValueError(f"unknown scaling {scaling!r}: one of {', '.join(_SCALINGS)}")
-        turns = torch.empty(max(rot // 2, 1), dtype=torch.int64)  # 2^-64 turns per position
+        turns = torch.empty(max(rot // 2, 1), dtype=torch.int64, device="cpu")  # 2^-64 turns per position
         mscale = _c.c_float()
         _abi.check(_abi.load().st_rope_turns(rot, base, _SCALINGS[scaling], factor, original, turns.data_ptr(),
                                              _c.byref(mscale)), "st_rope_turns")

@@ -338,3 +338,11 @@ def test_gradients_are_brought_to_aligned_rows():
         assert torch.equal(y, t) and y.data_ptr() % 16 == 0 and y.stride(-1) == 1
         assert all(n == 1 or (s >= 64 and s % 8 == 0) for n, s in zip(y.shape[:-1], y.stride()))
     assert lm._as_rows(even) is even and lm._as_rows(even.transpose(1, 2)).data_ptr() == even.data_ptr()
+
+
+def test_rope_table_under_a_default_device():
+    """The speeds are written on the host, whatever device new tensors have by default."""
+    want = bsf.RopeTable(64, scaling="yarn", factor=4.0, device="cpu")
+    with torch.device("meta"):
+        got = bsf.RopeTable(64, scaling="yarn", factor=4.0, device="cpu")
+    assert got.turns.device.type == "cpu" and torch.equal(got.turns, want.turns) and got.mscale == want.mscale
