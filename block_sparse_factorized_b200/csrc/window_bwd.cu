@@ -14,17 +14,19 @@
 // chunks whose fp32 partial sums a third launch adds in order.
 //
 // One CTA an SM, persistent: a producer warp (TMA), a warp that issues the products, two softmax
-// warpgroups with 64 columns each.  The issuing warp walks its steps as a whole and an elected lane issues:
-// in a loop of one lane whose branches depend on loaded values the products' operands stay out of the
-// uniform registers, and the issue itself bounds the kernel (dk_dv 489 us, walking and electing 447).
+// warpgroups with 64 columns each.  The issuing warp walks its steps as a whole and an elected lane issues
+// (dk_dv 447 us; a loop of one lane, whose branches depend on loaded values, 489).
 //
 // Measured, bf16, n = 12288, 2 x 16 heads on 4, window 1024, 16 sinks (10 d operations a pair, of 1616
 // TFLOP/s for a library product):
-//   d 128   840 us, 596 TFLOP/s: preparation 43, dk_dv 460, dq 392 (partly beside dk_dv), join 6
-//   d 64    645 us, 389 TFLOP/s: preparation 23, dk_dv 360, dq 308, join 5
-// and 1 x 16 heads over the whole past at d 128: 1805 us, 857 TFLOP/s.  Bound by the chains of a step: at
-// d = 128 a step of dk_dv takes 3400 cycles (2048 of products, which shared memory feeds at its limit), one
-// of dq 2850 (1536); at d = 64 the softmax warps take longer than the products.
+//   d 128   841 us, 596 TFLOP/s: preparation 43, dk_dv 460, dq 392 (partly beside dk_dv), join 6
+//   d 64    644 us, 389 TFLOP/s: preparation 23, dk_dv 360, dq 308, join 5
+// and 1 x 16 heads over the whole past at d 128: 1832 us, 844 TFLOP/s.  Bound by the chains of a step: at
+// d = 128 a step of dk_dv takes 3400 cycles for 2048 of products (the tensor pipe is 56% busy, shared
+// memory's 57%): S, dP, dV and dK fill TMEM, so S^T of the next step waits for dV, which reads P from its
+// columns.  One of dq takes 2850 for 1536; at d = 64 the softmax warps take longer than the products.
+// A tile of sinks is a whole step for its few live keys: in turns on a warm card 861 us with 16 sinks and
+// 778 without (d 64: 654, 589); 4 x 8 heads on 2 of 4096 rows, d 64, window 256: 130 with 4 sinks, 103 without.
 //
 // fp16 has a narrow range: P is kept 2^14 larger, and dS scaled by a power of two per (batch, key
 // head) from the bound |dS| <= 2 max|dO_i| max|v_j| / sqrt d, so that neither overflows nor fades; the

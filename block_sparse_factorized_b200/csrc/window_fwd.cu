@@ -23,10 +23,13 @@
 // the exponentials 1024 cycles of the special-function units.
 //
 // Measured, bf16, n = 12288 (of 1616 TFLOP/s for a library product):
-//   d 128, 2 x 16 heads on 4, window 1024, 16 sinks   288 us    695 TFLOP/s
-//   d 128, 1 x 16 heads on 4, the whole past          592 us   1045 TFLOP/s
-//   d 64,  2 x 16 heads on 4, window 1024, 16 sinks   250 us    400 TFLOP/s
-// and a padded batch (lengths 4099, 2300, 1200, 1; 16 heads on 4, d 128, window 1024) 100 us.
+//   d 128, 2 x 16 heads on 4, window 1024, 16 sinks   289 us    694 TFLOP/s
+//   d 128, 1 x 16 heads on 4, the whole past          598 us   1034 TFLOP/s
+//   d 64,  2 x 16 heads on 4, window 1024, 16 sinks   254 us    395 TFLOP/s
+//   d 64,  1 x 16 heads on 4, the whole past          551 us    561 TFLOP/s
+// and a padded batch (lengths 4099, 2300, 1200, 1; 16 heads on 4, d 128, window 1024) 105 us.  The tile of
+// the sinks is a whole step for its few live keys: in turns, on a card warm from the backward, 307 us with
+// 16 sinks and 281 without at d 128, 261 and 238 at d 64.
 // Bound at d = 64 by the softmax warps: 4400 cycles a pair of tiles, 2050 of them exponentials, the rest
 // latencies of two warps a scheduler (TMEM loads and stores, barriers); starting one sub later changes
 // nothing.  At d = 128 by the chain softmax -> P V -> S of a sub, 4900 cycles a step, 1800 of them waiting

@@ -336,7 +336,8 @@ ST_API st_status_t st_window_upload(st_window_t *window, st_stream_t stream);
  * a bounded wait gave up, ST_ERR_BAD_PAGE if a block table named a page outside the cache.  The
  * error word is shared by every call made with the handle, on any stream. */
 ST_API st_status_t st_window_check(st_window_t *window, st_stream_t stream);
-/* Release the handle (NULL is a no-op).  Work that uses it must have completed. */
+/* Release the handle (NULL is a no-op).  Work that uses it must have completed, and captured graphs of
+ * its calls hold the error word's address: they must not be replayed after this. */
 ST_API void st_window_destroy(st_window_t *window);
 
 /* Shapes of a window call.  q, o, dO, dq: [batch, heads, nq, d]; k, v, dk, dv: [batch, kv_heads,
@@ -486,9 +487,10 @@ ST_API st_status_t st_paged_append(const void *q, const void *k, const void *v, 
  * token's included (clamped to 0 .. max_pages * page_size), so the query stands at lens - 1.  A request
  * of length 0 gets O = 0, lse = -inf.  A key whose page is outside 0 .. num_pages - 1 is not seen, and
  * the window's error word records it (ST_ERR_BAD_PAGE from st_window_check).  Cache rows that are
- * not seen are not used, whatever they hold; a score of NaN or +inf gives NaN in O and lse.  d: 64 or 128;
- * dtype: ST_BF16 or ST_FP16; heads / kv_heads <= 64; requests <= 8192; page_size a multiple of 16;
- * max_pages * page_size <= 2^30.  o, lse and the workspace must not overlap each other or an input.  The
+ * not seen are not used, whatever they hold; a score of NaN or +inf gives NaN in O and lse.  For the
+ * second product the probabilities are rounded to the inputs' type; with ST_BF16 and heads / kv_heads <= 8
+ * they keep 16 bits (two bf16 parts).  d: 64 or 128; dtype: ST_BF16 or ST_FP16; heads / kv_heads <= 64;
+ * requests <= 8192; page_size a multiple of 16; max_pages * page_size <= 2^30.  o, lse and the workspace must not overlap each other or an input.  The
  * order of the sums depends on lens and on the device only: the same inputs give the same bits.
  * Errors: ST_ERR_INVALID_ARG, ST_ERR_UNSUPPORTED, ST_ERR_ALIGNMENT, ST_ERR_NOT_UPLOADED,
  * ST_ERR_WORKSPACE, ST_ERR_CUDA. */
