@@ -371,7 +371,9 @@ ST_API st_status_t st_window_fwd(const void *q, const void *k, const void *v, co
 /* Backward with recomputation from q, k and the saved lse: dq, dk, dv (every element written;
  * padding rows and unseen keys get 0, whatever dO, O and lse hold there).  The sums run in a fixed
  * order: the same inputs give the same bits.  dS (and P) are rounded to the inputs' type for their
- * products; with ST_FP16 they are scaled by powers of two that keep them in range, per key head.
+ * products; with ST_FP16 they are scaled by powers of two that keep them in range, per key head.  A NaN or
+ * an infinity in a row before lens[b] (dO, O and lse included) may reach any gradient of its batch element
+ * and group, those of unseen keys too.
  * dq, dk, dv and the workspace must not overlap each other or an input.
  * Errors as for the forward, and ST_ERR_WORKSPACE. */
 ST_API size_t st_window_bwd_workspace_bytes(const st_window_desc_t *desc, const st_window_t *window);
